@@ -24,6 +24,8 @@ GDN_QK_L2NORM = 1
 GDN_STATE_ONLY = 2
 GDN_PRECISE = 4
 GDN_SCALAR_DECAY = 8
+GDN_HEAD_DECAY = 16
+GDN_KEEP_STATE = 32
 
 ERROR_NAMES = {
     GDN_ERR_ARG: "GDN_ERR_ARG", GDN_ERR_SHAPE: "GDN_ERR_SHAPE", GDN_ERR_ALIGN: "GDN_ERR_ALIGN",
@@ -46,6 +48,17 @@ class GdnDims(ctypes.Structure):
     ]
 
 
+class GdnVerifyDims(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("n_draft", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("target_stride", ctypes.c_int64),
+        ("draft_stride", ctypes.c_int64),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, code: int, where: str, message: str):
         self.code = code
@@ -62,6 +75,9 @@ SIGNATURES = {
     "gdn_replay_noalloc": ([_PD, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "gdn_chunk_operator": ([_PD, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "gdn_compose": ([_PD, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "gdn_linear_attn": ([_PD, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "gdn_decode": ([_PD, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "gdn_verify_draft": ([ctypes.POINTER(GdnVerifyDims), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "gdn_get_status": ([_VP], ctypes.c_int),
     "gdn_last_error": ([], ctypes.c_char_p),
     "gdn_workspace_bytes": ([_PD], ctypes.c_size_t),

@@ -176,6 +176,169 @@ def gdn_compose(T_list, Slocal_list, S_in=None, *, S_out=None, stream=None):
     return S_out
 
 
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {ref.device}")
+
+
+def _on(device, stream):
+    """Context of a call on ``device`` and ``stream`` (None: its current stream): what the call
+    allocates then belongs to the stream that the kernels run on."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    return torch.cuda.stream(stream)
+
+
+def gdn_linear_attn(q, k, v, log_decay, cu_seqlens, S0=None, *, O_out=None, S_out=None, scale=1.0,
+                    state_only=False, stream=None):
+    """Linear attention with a decay for each head over packed prompts (see gdn.h):
+    S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T, o_t = S_t (scale q_t).
+
+    q, k: [T, h_k, d_k]; v: [T, h_v, d_v] (all bf16 or all fp32; q may be None with
+    ``state_only``); log_decay: fp32 [h_v]; cu_seqlens: int32 [n + 1] on the device; S0: fp32
+    [n, h_v, d_v, d_k] or None.  Returns (O, S) as gdn_replay does."""
+    lib = _lib.load()
+    T, h_k, d_k = k.shape
+    h_v, d_v = v.shape[1], v.shape[2]
+    n = cu_seqlens.shape[0] - 1
+    dt = k.dtype
+    if dt not in _DTYPE:
+        raise ValueError(f"unsupported dtype {dt}")
+    if q is None and not state_only:
+        raise ValueError("q may be None only with state_only")
+    _need_cuda("q", q, dt, (T, h_k, d_k))
+    _need_cuda("k", k, dt)
+    _need_cuda("v", v, dt, (T, h_v, d_v))
+    _need_cuda("log_decay", log_decay, torch.float32, (h_v,))
+    _need_cuda("cu_seqlens", cu_seqlens, torch.int32, (n + 1,))
+    _need_cuda("S0", S0, torch.float32, (n, h_v, d_v, d_k))
+    _need_cuda("S_out", S_out, torch.float32, (n, h_v, d_v, d_k))
+    _need_cuda("O_out", O_out, dt, (T, h_v, d_v))
+    _same_device(k, q=q, v=v, log_decay=log_decay, cu_seqlens=cu_seqlens, S0=S0, S_out=S_out, O_out=O_out)
+    with _on(k.device, stream):
+        if S_out is None:
+            S_out = torch.empty((n, h_v, d_v, d_k), dtype=torch.float32, device=k.device)
+        if state_only:
+            O_out = None
+        elif O_out is None:
+            O_out = torch.empty((T, h_v, d_v), dtype=dt, device=k.device)
+        dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], _lib.GDN_STATE_ONLY if state_only else 0,
+                            float(scale))
+        rc = lib.gdn_linear_attn(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens),
+                                 _ptr(S0), _ptr(O_out), _ptr(S_out), _stream_handle(stream, k.device))
+    _lib.check(rc, "gdn_linear_attn")
+    return O_out, S_out
+
+
+def gdn_decode(q, k, v, g, beta, S_pool, slots=None, *, counts=None, O_out=None, l2norm_qk=True, scale=1.0,
+               state_only=False, keep_state=False, scalar_decay=False, head_decay=False, stream=None):
+    """One token, or a window of tokens, for each request on its state in ``S_pool`` (see gdn.h).
+
+    q, k: [n * window, h_k, d_k]; v: [n * window, h_v, d_v], request after request (all bf16 or
+    all fp32; q may be None with ``state_only``); g, beta: fp32 [n * window, h_v] (``head_decay``:
+    g is the log decay [h_v] and beta None); S_pool: fp32 [n_slots, h_v, d_v, d_k], updated in
+    place unless ``keep_state``; slots: int32 [n] on the device (negative: padding) or None, then
+    n = n_slots; counts: int32 [n] on the device, the tokens of each window that count, or None.
+    Returns O [n * window, h_v, d_v] in the input dtype, None with ``state_only``.  Rows that do
+    not count are left as they were (undefined when O is allocated here)."""
+    lib = _lib.load()
+    T, h_k, d_k = k.shape
+    h_v, d_v = v.shape[1], v.shape[2]
+    n_slots = S_pool.shape[0]
+    n = n_slots if slots is None else slots.shape[0]
+    dt = k.dtype
+    if dt not in _DTYPE:
+        raise ValueError(f"unsupported dtype {dt}")
+    if q is None and not state_only:
+        raise ValueError("q may be None only with state_only")
+    if n == 0 and T:
+        raise ValueError(f"{T} tokens of no requests")
+    _need_cuda("q", q, dt, (T, h_k, d_k))
+    _need_cuda("k", k, dt)
+    _need_cuda("v", v, dt, (T, h_v, d_v))
+    _need_cuda("g", g, torch.float32, (h_v,) if head_decay else (T, h_v))
+    _need_cuda("beta", beta, torch.float32, (T, h_v))
+    _need_cuda("S_pool", S_pool, torch.float32, (n_slots, h_v, d_v, d_k))
+    _need_cuda("slots", slots, torch.int32, (n,))
+    _need_cuda("counts", counts, torch.int32, (n,))
+    _need_cuda("O_out", O_out, dt, (T, h_v, d_v))
+    _same_device(k, q=q, v=v, g=g, beta=beta, S_pool=S_pool, slots=slots, counts=counts, O_out=O_out)
+    flags = (_lib.GDN_QK_L2NORM if l2norm_qk else 0) | (_lib.GDN_STATE_ONLY if state_only else 0) \
+        | (_lib.GDN_SCALAR_DECAY if scalar_decay else 0) | (_lib.GDN_HEAD_DECAY if head_decay else 0) \
+        | (_lib.GDN_KEEP_STATE if keep_state else 0)
+    with _on(k.device, stream):
+        if state_only:
+            O_out = None
+        elif O_out is None:
+            O_out = torch.empty((T, h_v, d_v), dtype=dt, device=k.device)
+        dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], flags, float(scale))
+        rc = lib.gdn_decode(ctypes.byref(dims), n_slots, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(slots),
+                            _ptr(counts), _ptr(S_pool), _ptr(O_out), _stream_handle(stream, k.device))
+    _lib.check(rc, "gdn_decode")
+    return O_out
+
+
+def _prob_rows(name, t, shape):
+    """Element stride between the rows of probabilities t [n, rows, vocab] (a vocabulary slice of
+    padded rows will do; the rows must be evenly spaced)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return shape[2]
+    n, rows, _ = shape
+    step = t.stride(1) if rows > 1 else t.stride(0)
+    if t.stride(2) != 1 or (n > 1 and t.stride(0) != rows * step):
+        raise ValueError(f"{name} must have evenly spaced rows of consecutive entries")
+    return step
+
+
+def gdn_verify_draft(target, drafted, uniforms, draft=None, draft_lens=None, *, counts_out=None, tokens_out=None,
+                     stream=None):
+    """Drafted tokens against the target's probabilities, from given random numbers (see gdn.h).
+
+    target: [n, n_draft + 1, vocab] fp32 or bf16; draft: [n, n_draft, vocab] of the same dtype, or
+    None when the drafts were chosen outright; drafted: int32 [n, n_draft]; uniforms: fp32
+    [n, n_draft + 1] in [0, 1); draft_lens: int32 [n] (negative: padding) or None.
+    Returns (counts, tokens): counts int32 [n], the emitted tokens of each request (accepted
+    drafts + 1), and tokens int32 [n, n_draft + 1], those tokens followed by -1."""
+    lib = _lib.load()
+    n, n_draft = drafted.shape
+    if target.dim() != 3:
+        raise ValueError("target must be [n, n_draft + 1, vocab]")
+    vocab = target.shape[2]
+    if target.dtype not in _DTYPE:
+        raise ValueError(f"unsupported dtype {target.dtype}")
+    target_stride = _prob_rows("target", target, (n, n_draft + 1, vocab))
+    draft_stride = 0
+    if draft is not None:
+        if draft.dtype != target.dtype:
+            raise ValueError(f"draft must be {target.dtype}, got {draft.dtype}")
+        draft_stride = _prob_rows("draft", draft, (n, n_draft, vocab))
+    _need_cuda("drafted", drafted, torch.int32)
+    _need_cuda("uniforms", uniforms, torch.float32, (n, n_draft + 1))
+    _need_cuda("draft_lens", draft_lens, torch.int32, (n,))
+    _need_cuda("counts_out", counts_out, torch.int32, (n,))
+    _need_cuda("tokens_out", tokens_out, torch.int32, (n, n_draft + 1))
+    _same_device(target, draft=draft, drafted=drafted, uniforms=uniforms, draft_lens=draft_lens,
+                 counts_out=counts_out, tokens_out=tokens_out)
+    with _on(target.device, stream):
+        if counts_out is None:
+            counts_out = torch.empty((n,), dtype=torch.int32, device=target.device)
+        if tokens_out is None:
+            tokens_out = torch.empty((n, n_draft + 1), dtype=torch.int32, device=target.device)
+        dims = _lib.GdnVerifyDims(n, n_draft, vocab, _DTYPE[target.dtype], target_stride, draft_stride)
+        rc = lib.gdn_verify_draft(ctypes.byref(dims), _ptr(target), _ptr(draft), _ptr(drafted), _ptr(draft_lens),
+                                  _ptr(uniforms), _ptr(counts_out), _ptr(tokens_out),
+                                  _stream_handle(stream, target.device))
+    _lib.check(rc, "gdn_verify_draft")
+    return counts_out, tokens_out
+
+
 def gdn_get_status(stream=None, device=None):
     """Synchronise the stream; raise GdnError if the device recorded an error."""
     lib = _lib.load()

@@ -36,6 +36,9 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 __device__ int g_status;  // sticky per-device status (one copy per device that loads the library)
 
+constexpr int kMaxGridY = 65535;    // v-heads of one launch of the prompt and decode kernels
+constexpr int kMaxVocab = 1 << 19;  // sums of 2^-44 fixed-point probabilities stay below 2^63
+
 int check_head_dims(const gdn_dims* d) {
   if (d->h_k <= 0 || d->h_v <= 0) return fail(GDN_ERR_ARG, "h_k and h_v must be positive");
   if (d->h_v % d->h_k != 0) return fail(GDN_ERR_SHAPE, "h_v (%d) must be a multiple of h_k (%d)", d->h_v, d->h_k);
@@ -266,6 +269,116 @@ int gdn_compose(const gdn_dims* dims, int32_t K, const float* const* T, const fl
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = compose_tc_supported(p) ? launch_compose_tc(p, st) : launch_compose_simt(p, st);
   if (e != cudaSuccess) return cuda_fail(e, "gdn_compose launch");
+  return GDN_OK;
+}
+
+int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                    const int32_t* cu_seqlens, const float* S0, void* O_out, float* S_out, void* stream) {
+  g_last_error.clear();
+  if (!dims) return fail(GDN_ERR_ARG, "dims is NULL");
+  if (dims->flags & ~GDN_STATE_ONLY) return fail(GDN_ERR_ARG, "gdn_linear_attn takes GDN_STATE_ONLY only, got 0x%x", dims->flags);
+  int rc = check_token_dims(dims);
+  if (rc) return rc;
+  if (dims->h_v > kMaxGridY) return fail(GDN_ERR_UNSUPPORTED, "h_v=%d above %d", dims->h_v, kMaxGridY);
+  const bool state_only = dims->flags & GDN_STATE_ONLY;
+  if (dims->n_seqs == 0) return GDN_OK;
+  if (!cu_seqlens || !S_out || !log_decay) return fail(GDN_ERR_ARG, "cu_seqlens, log_decay and S_out are required");
+  if (!state_only && !O_out) return fail(GDN_ERR_ARG, "O_out is NULL without GDN_STATE_ONLY");
+  if (dims->total_tokens > 0 && ((!q && !state_only) || !k || !v))
+    return fail(GDN_ERR_ARG, "q (unless GDN_STATE_ONLY), k and v are required when total_tokens > 0");
+  const void* p16[] = {q, k, v, O_out, S0, S_out};
+  for (const void* ptr : p16)
+    if (ptr && !aligned(ptr, 16)) return fail(GDN_ERR_ALIGN, "q, k, v, O, S0 and S_out must be 16-byte aligned");
+  if (!aligned(log_decay, 4) || !aligned(cu_seqlens, 4))
+    return fail(GDN_ERR_ALIGN, "log_decay and cu_seqlens must be 4-byte aligned");
+  LinearParams p{};
+  p.q = q; p.k = k; p.v = v; p.log_decay = log_decay; p.cu = cu_seqlens; p.S0 = S0;
+  p.O = state_only ? nullptr : O_out; p.S_out = S_out;
+  p.n_seqs = dims->n_seqs; p.total_tokens = dims->total_tokens;
+  p.h_k = dims->h_k; p.h_v = dims->h_v; p.d_k = dims->d_k; p.d_v = dims->d_v;
+  p.write_O = state_only ? 0 : 1; p.scale = dims->scale;
+  p.status = device_status_word();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_linear_simt(p, dims->dtype == GDN_BF16, st);
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_linear_attn launch");
+  return GDN_OK;
+}
+
+int gdn_decode(const gdn_dims* dims, int32_t n_slots, const void* q, const void* k, const void* v, const float* g,
+               const float* beta, const int32_t* slots, const int32_t* counts, float* S_pool, void* O_out,
+               void* stream) {
+  g_last_error.clear();
+  if (!dims) return fail(GDN_ERR_ARG, "dims is NULL");
+  gdn_dims base = *dims;
+  base.flags &= ~(GDN_HEAD_DECAY | GDN_KEEP_STATE);
+  int rc = check_token_dims(&base);
+  if (rc) return rc;
+  const uint32_t fl = dims->flags;
+  const bool state_only = fl & GDN_STATE_ONLY, keep = fl & GDN_KEEP_STATE, head = fl & GDN_HEAD_DECAY;
+  if (fl & GDN_PRECISE) return fail(GDN_ERR_ARG, "gdn_decode takes no GDN_PRECISE (every sum is in fp32)");
+  if (state_only && keep) return fail(GDN_ERR_ARG, "GDN_STATE_ONLY with GDN_KEEP_STATE leaves nothing to do");
+  if (head && (fl & GDN_SCALAR_DECAY)) return fail(GDN_ERR_ARG, "GDN_HEAD_DECAY and GDN_SCALAR_DECAY exclude each other");
+  if (dims->h_v > kMaxGridY) return fail(GDN_ERR_UNSUPPORTED, "h_v=%d above %d", dims->h_v, kMaxGridY);
+  if (n_slots < 0) return fail(GDN_ERR_ARG, "negative n_slots");
+  if (dims->n_seqs == 0 || dims->total_tokens == 0) return GDN_OK;
+  if (dims->total_tokens % dims->n_seqs)
+    return fail(GDN_ERR_SHAPE, "total_tokens (%d) must be n_seqs (%d) windows of one length", dims->total_tokens, dims->n_seqs);
+  if (!slots && dims->n_seqs > n_slots)
+    return fail(GDN_ERR_SHAPE, "%d requests on %d slots without a slot list", dims->n_seqs, n_slots);
+  if (!S_pool && n_slots > 0) return fail(GDN_ERR_ARG, "S_pool is required");
+  if (!k || !v || !g || (!q && !state_only)) return fail(GDN_ERR_ARG, "q (unless GDN_STATE_ONLY), k, v and g are required");
+  if (head ? beta != nullptr : beta == nullptr)
+    return fail(GDN_ERR_ARG, "beta is required, and must be NULL with GDN_HEAD_DECAY");
+  if (!state_only && !O_out) return fail(GDN_ERR_ARG, "O_out is NULL without GDN_STATE_ONLY");
+  const void* p16[] = {q, k, v, O_out, S_pool};
+  for (const void* ptr : p16)
+    if (ptr && !aligned(ptr, 16)) return fail(GDN_ERR_ALIGN, "q, k, v, O and S_pool must be 16-byte aligned");
+  if (!aligned(g, 4) || !aligned(beta, 4) || !aligned(slots, 4) || !aligned(counts, 4))
+    return fail(GDN_ERR_ALIGN, "g, beta, slots and counts must be 4-byte aligned");
+  DecodeParams p{};
+  p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.slots = slots; p.counts = counts; p.S = S_pool;
+  p.O = state_only ? nullptr : O_out;
+  p.n = dims->n_seqs; p.window = dims->total_tokens / dims->n_seqs; p.n_slots = n_slots;
+  p.h_k = dims->h_k; p.h_v = dims->h_v; p.d_k = dims->d_k; p.d_v = dims->d_v;
+  p.family = head ? kHeadDecay : (fl & GDN_SCALAR_DECAY) ? kScalarDecay : kDelta;
+  p.l2norm = (fl & GDN_QK_L2NORM) ? 1 : 0; p.state_only = state_only ? 1 : 0; p.keep = keep ? 1 : 0;
+  p.scale = dims->scale;
+  p.status = device_status_word();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  const cudaError_t e = launch_decode(p, dims->dtype == GDN_BF16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_decode launch");
+  return GDN_OK;
+}
+
+int gdn_verify_draft(const gdn_verify_dims* dims, const void* target, const void* draft, const int32_t* drafted,
+                     const int32_t* draft_lens, const float* uniforms, int32_t* counts_out, int32_t* tokens_out,
+                     void* stream) {
+  g_last_error.clear();
+  if (!dims) return fail(GDN_ERR_ARG, "dims is NULL");
+  if (dims->n_seqs < 0 || dims->n_draft < 0) return fail(GDN_ERR_ARG, "negative n_seqs or n_draft");
+  if (dims->vocab <= 0) return fail(GDN_ERR_ARG, "vocab must be positive");
+  if (dims->dtype != GDN_F32 && dims->dtype != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d", dims->dtype);
+  if (dims->vocab > kMaxVocab) return fail(GDN_ERR_UNSUPPORTED, "vocab=%d above %d", dims->vocab, kMaxVocab);
+  if (dims->target_stride < dims->vocab || (draft && dims->draft_stride < dims->vocab))
+    return fail(GDN_ERR_SHAPE, "a row stride is below vocab (%d)", dims->vocab);
+  if (dims->n_seqs == 0) return GDN_OK;
+  if (!target || !uniforms || !counts_out || !tokens_out)
+    return fail(GDN_ERR_ARG, "target, uniforms, counts_out and tokens_out are required");
+  if (dims->n_draft > 0 && !drafted) return fail(GDN_ERR_ARG, "drafted is required when n_draft > 0");
+  const size_t es = dims->dtype == GDN_BF16 ? 2 : 4;
+  if (!aligned(target, es) || !aligned(draft, es)) return fail(GDN_ERR_ALIGN, "target and draft must be aligned to their type");
+  if (!aligned(drafted, 4) || !aligned(draft_lens, 4) || !aligned(uniforms, 4) || !aligned(counts_out, 4) || !aligned(tokens_out, 4))
+    return fail(GDN_ERR_ALIGN, "drafted, draft_lens, uniforms, counts_out and tokens_out must be 4-byte aligned");
+  VerifyParams p{};
+  p.target = target; p.draft = dims->n_draft > 0 ? draft : nullptr; p.drafted = drafted; p.draft_lens = draft_lens;
+  p.uniforms = uniforms; p.counts = counts_out; p.tokens = tokens_out;
+  p.target_stride = dims->target_stride; p.draft_stride = dims->draft_stride;
+  p.n = dims->n_seqs; p.n_draft = dims->n_draft; p.vocab = dims->vocab;
+  p.status = device_status_word();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  const cudaError_t e = launch_verify(p, dims->dtype == GDN_BF16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_verify_draft launch");
   return GDN_OK;
 }
 

@@ -101,6 +101,76 @@ cudaError_t launch_state_tc(const CUtensorMap& mk, const CUtensorMap& mv, const 
 bool chunkop_tc_supported(const SimtParams& p, int bf16);
 cudaError_t launch_chunkop_tc(const SimtParams& p, int bf16, cudaStream_t stream);
 
+// Linear attention with a decay for each head over packed prompts (gdn_linear_attn).
+struct LinearParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* log_decay;  // [h_v]
+  const int32_t* cu;
+  const float* S0;  // or null
+  void* O;
+  float* S_out;
+  int* status;
+  int n_seqs, total_tokens, h_k, h_v, d_k, d_v;
+  int write_O;
+  float scale;
+};
+cudaError_t launch_linear_simt(const LinearParams& p, int bf16, cudaStream_t stream);
+
+// S <- lambda^n S + D of a carried state, lambda = exp(g).  A factor near 1 stored in fp32 is off by
+// up to 2^-25, always the same way, and a long prompt multiplies by it hundreds of times; the step
+// S + (lambda^n - 1) S is off by 2^-24 |lambda^n - 1| instead, plus the sum's own unbiased rounding.
+// Below 1/2 the factor itself is exact enough (and S + (f - 1) S would cancel).
+struct DecayStep {
+  float f, f1;
+  bool near1;
+  __device__ __forceinline__ float operator()(float s, float d) const {
+    return near1 ? fmaf(s, f1, s + d) : fmaf(s, f, d);
+  }
+};
+__device__ __forceinline__ DecayStep decay_step(float g, int n) {
+  DecayStep r;
+  r.f = expf((float)n * g);
+  r.f1 = expm1f((float)n * g);
+  r.near1 = r.f1 >= -0.5f;
+  return r;
+}
+
+// Recurrent form on a pool of states (gdn_decode).
+enum : int { kDelta = 0, kScalarDecay = 1, kHeadDecay = 2 };
+struct DecodeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;      // null for kHeadDecay
+  const int32_t* slots;   // or null: request i on slot i
+  const int32_t* counts;  // or null: the whole window
+  float* S;               // [n_slots][h_v][d_v][d_k]
+  void* O;
+  int* status;
+  int n, window, n_slots, h_k, h_v, d_k, d_v;
+  int family, l2norm, state_only, keep;
+  float scale;
+};
+cudaError_t launch_decode(const DecodeParams& p, int bf16, cudaStream_t stream);
+
+// Verification of drafted tokens (gdn_verify_draft).
+struct VerifyParams {
+  const void* target;
+  const void* draft;          // or null
+  const int32_t* drafted;     // [n][n_draft]
+  const int32_t* draft_lens;  // or null
+  const float* uniforms;      // [n][n_draft + 1]
+  int32_t* counts;            // [n]
+  int32_t* tokens;            // [n][n_draft + 1]
+  int* status;
+  int64_t target_stride, draft_stride;  // elements between consecutive rows
+  int n, n_draft, vocab;
+};
+cudaError_t launch_verify(const VerifyParams& p, int bf16, cudaStream_t stream);
+
 // Sticky status word of the current device (device pointer).
 int* device_status_word();
 

@@ -75,6 +75,8 @@ extern "C" {
  * (prod alpha_t) I.  Accepted by gdn_replay, gdn_replay_noalloc and
  * gdn_chunk_operator (whose T_out is then that scaled identity). */
 #define GDN_SCALAR_DECAY 8u
+#define GDN_HEAD_DECAY 16u /* gdn_decode: one decay per v-head, S_t = lambda_h S_{t-1} + v_t k_t^T */
+#define GDN_KEEP_STATE 32u /* gdn_decode: outputs only, the states stay as they are */
 
 typedef struct {
   int32_t n_seqs;       /* packed sequences (replay tails, or chunks for gdn_chunk_operator) */
@@ -195,6 +197,94 @@ int gdn_chunk_operator(const gdn_dims* dims, const void* k, const float* g, cons
  */
 int gdn_compose(const gdn_dims* dims, int32_t K, const float* const* T, const float* const* Slocal,
                 const float* S_in, float* S_out, void* stream);
+
+/*
+ * gdn_linear_attn -- linear attention with a decay for each head, over packed prompts.
+ * Source: the scalar-transition family that "LinearKV: One Cached State Suffices
+ * for Position-Independent Caching in Hybrid LLMs" (composition passage) sets
+ * beside the delta rule, with a transition that belongs to the head alone:
+ *     S_t = lambda_h S_{t-1} + v_t k_t^T,   o_t = S_t (scale * q_t),   lambda_h = exp(log_decay[h]).
+ *   dims        as gdn_replay's; the only flag taken is GDN_STATE_ONLY (q and k are used as given)
+ *   q, k, v     inputs in `dims->dtype`, layouts above (q may be NULL with GDN_STATE_ONLY)
+ *   log_decay   fp32 device [h_v], <= 0 (0: no decay; -inf: each token's state is its own)
+ *   cu_seqlens  int32 device [n_seqs + 1]; malformed ranges are skipped and reported as in gdn_replay
+ *   S0          fp32 [n_seqs][h_v][d_v][d_k] or NULL (zero); a sequence of no tokens returns it
+ *   O_out       [total_tokens][h_v][d_v] in `dims->dtype`, NULL iff GDN_STATE_ONLY; rows outside
+ *               every sequence's range are not written
+ *   S_out       fp32 [n_seqs][h_v][d_v][d_k]; may alias S0
+ * The state is carried in fp32 and at fp32 accuracy whatever the inputs' type.
+ */
+int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                    const int32_t* cu_seqlens, const float* S0, void* O_out, float* S_out, void* stream);
+
+/*
+ * gdn_decode -- the recurrent form: one token, or a short window of tokens, for
+ * each of n_seqs requests whose states live in a pool.
+ * Source: "Tail-Replay: ..." section 2, Eq. (1), token by token (delta rule; with
+ * GDN_SCALAR_DECAY or GDN_HEAD_DECAY the scalar-transition families), readout with
+ * the updated state as in gdn_replay.
+ *   dims        n_seqs requests; total_tokens = n_seqs * window: request i's tokens are rows
+ *               [i * window, (i + 1) * window) of q, k, v, g, beta and O
+ *   n_slots     states in the pool
+ *   g, beta     fp32 [total_tokens][h_v]; with GDN_HEAD_DECAY g is the log decay [h_v] and beta NULL
+ *   slots       int32 device [n_seqs]: each request's state in the pool; NULL: request i has state i.
+ *               A negative slot is padding: nothing of that request is read or written.
+ *   counts      int32 device [n_seqs]: how many of the window's tokens count, 0 to window; NULL: all.
+ *               The rows behind them are not read, and their outputs are left as they were.
+ *   S_pool      fp32 [n_slots][h_v][d_v][d_k], updated in place (read only with GDN_KEEP_STATE)
+ *   O_out       [total_tokens][h_v][d_v] in `dims->dtype`; NULL iff GDN_STATE_ONLY
+ * Flags: GDN_QK_L2NORM, GDN_STATE_ONLY, GDN_SCALAR_DECAY, GDN_HEAD_DECAY, GDN_KEEP_STATE.
+ * Speculative decoding runs a window with GDN_KEEP_STATE (the output of every position, the states
+ * untouched), verifies the drafts (gdn_verify_draft) and then runs the same window with
+ * GDN_STATE_ONLY and the verification's counts: a recurrent state cannot be cut back like a
+ * key-value cache, so it is advanced by exactly the tokens that stand.
+ * A slot past the pool, a count outside the window, or a slot that an earlier request of the call
+ * already updates: that request is skipped and GDN_ERR_SHAPE reported through gdn_get_status.
+ * No scratch memory; the call can be captured into a graph and replayed with new contents.
+ */
+int gdn_decode(const gdn_dims* dims, int32_t n_slots, const void* q, const void* k, const void* v, const float* g,
+               const float* beta, const int32_t* slots, const int32_t* counts, float* S_pool, void* O_out,
+               void* stream);
+
+typedef struct {
+  int32_t n_seqs;        /* requests */
+  int32_t n_draft;       /* drafted tokens per request (the most, with draft_lens) */
+  int32_t vocab;         /* entries of a probability row, at most 524288 */
+  int32_t dtype;         /* of target and draft: GDN_F32 or GDN_BF16 */
+  int64_t target_stride; /* elements between consecutive rows of target, at least vocab */
+  int64_t draft_stride;  /* the same of draft (ignored when draft is NULL) */
+} gdn_verify_dims;
+
+/*
+ * gdn_verify_draft -- drafted tokens against the target's probabilities, from given
+ * random numbers (speculative sampling: the emitted tokens follow the target's distribution).
+ * The pages have no counterpart; the call decides how many tokens of a window gdn_decode commits.
+ *   target      [n_seqs][n_draft + 1][vocab] probabilities: row j is the target's distribution of the
+ *               token at draft position j, row n_draft (or a request's draft length) that behind the drafts
+ *   draft       [n_seqs][n_draft][vocab], the distributions the drafts were drawn from, or NULL when
+ *               the drafts were chosen outright (each with probability 1)
+ *   drafted     int32 [n_seqs][n_draft]
+ *   draft_lens  int32 [n_seqs], each request's drafts, 0 to n_draft; NULL: n_draft each.  Negative:
+ *               padding, nothing of that request is read or written.
+ *   uniforms    fp32 [n_seqs][n_draft + 1] in [0, 1): the first n_draft for the drafts, the last one
+ *               for the sampled token
+ * Request by request: draft j is accepted while u_j * q_j(x_j) < p_j(x_j), in exact arithmetic.  Behind
+ * the a accepted ones a token is sampled from the distribution max(p_a - q_a, 0) when draft a was
+ * rejected (p_a itself where that is zero throughout), from p_a when every draft was accepted: the
+ * lowest index whose inclusive sum of weights exceeds floor(u * sum), the weights whole multiples of
+ * 2^-44 (each probability clamped to [0, 1] and rounded down; NaN counts as 0), so that the order of
+ * summation cannot change the token.
+ *   counts_out  int32 [n_seqs]: a + 1, the emitted tokens -- and, in a window of the last token
+ *               followed by the drafts, the tokens that gdn_decode is to commit
+ *   tokens_out  int32 [n_seqs][n_draft + 1]: the accepted drafts, the sampled token, then -1.  Where
+ *               the row to sample from is zero throughout, the sampled token is -1.
+ * A draft length above n_draft: the request is skipped and GDN_ERR_SHAPE reported through
+ * gdn_get_status.  A drafted token outside the vocabulary is rejected and reported the same way.
+ * No scratch memory; the call can be captured into a graph.
+ */
+int gdn_verify_draft(const gdn_verify_dims* dims, const void* target, const void* draft, const int32_t* drafted,
+                     const int32_t* draft_lens, const float* uniforms, int32_t* counts_out, int32_t* tokens_out,
+                     void* stream);
 
 /*
  * gdn_get_status -- synchronise `stream`, then return and clear the sticky
