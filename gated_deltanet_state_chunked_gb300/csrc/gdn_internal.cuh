@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include "../../include/gdn.h"
@@ -74,6 +75,8 @@ cudaError_t launch_compose_simt(const ComposeParams& p, cudaStream_t stream);
 bool compose_tc_supported(const ComposeParams& p);
 cudaError_t launch_compose_tc(const ComposeParams& p, cudaStream_t stream);
 
+// The driver's tensor-map encoder (null if unavailable).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 // Tensor map of a 2D bf16 view [rows][cols] (cols contiguous) with boxes of 64 columns x
 // box_rows rows, 128-byte swizzle (the tile layout the tensor-core operands use); false if the
 // driver's encoder is unavailable or rejects the view.
@@ -116,6 +119,10 @@ struct LinearParams {
   int write_O;
   float scale;
 };
+// Tensor-core path (bf16 inputs, total_tokens > 0); workspace: linear_tc_workspace_bytes(), may be 0.
+bool linear_tc_supported(const LinearParams& p);
+size_t linear_tc_workspace_bytes(const LinearParams& p);
+cudaError_t launch_linear_tc(const LinearParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_linear_simt(const LinearParams& p, int bf16, cudaStream_t stream);
 
 // S <- lambda^n S + D of a carried state, lambda = exp(g).  A factor near 1 stored in fp32 is off by
