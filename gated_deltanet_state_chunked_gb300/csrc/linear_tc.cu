@@ -9,7 +9,7 @@
 // below 2^-60 (the quotient must not overflow): a head that decays that far inside a chunk then keeps
 // 2^-60 of its entering state where it should keep less, 1e-18 of its size.
 //
-// One CTA owns one (segment of a sequence, v-head) and walks its chunks.  Products per chunk, all
+// A work item is one (segment of a sequence, v-head): its chunks in order.  Products per chunk, all
 // M = N = 128 (N = 64 for head sizes up to 64), fp32 accumulators in TMEM:
 //   QK   Q K^T             A = Q, B = K (both K-major)                  8 MMAs
 //   QS   Q S^T             A = Q, B = S rounded to bf16 (K-major)       8
@@ -31,13 +31,17 @@
 //         and the first half of the outputs, group 1 the others.  (State only: 0-3 as 2, 3.)
 //   2, 3  values to A operands, quarters of 32 tokens in turn: weight, transpose (ldmatrix), split
 //   4, 5  the state: a thread owns half a row of S
-//   6     one warp issues QK, QS, PV, one KV, one loads the tiles two chunks ahead and stores the
-//         outputs from the stage of Q that they replace
+//   6     one warp issues QK, QS, PV, one KV, one loads the tiles ahead and stores the outputs from the
+//         stage of V that they replace, one fetches the work
 // Every hand-off is an mbarrier; every wait is bounded.
 //
 // A sequence longer than `seg_tokens` is cut into segments, so that a few long prompts fill the GPU:
 // the segments' own states first (KV only, from zero), then their entering states
 // (linear_carry_kernel), then every segment as above.
+//
+// One CTA per SM stays and takes item after item (clusterlaunchcontrol): the loads, products and tables
+// of the next item start while the last chunks of the one before are finished.  With several sequences
+// linear_plan_kernel lists the segments, longest first, once per call.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -58,25 +62,37 @@ using tcp::kWaitNs;
 constexpr int C = 128;           // tokens per chunk
 constexpr int NWARP = 28, NT = 32 * NWARP;
 constexpr int kRegsLaunch = 72;  // a thread's registers at launch, and (below) in its warpgroup's role
-constexpr int kRegsRows = 72, kRegsSplit = 56, kRegsState = 112, kRegsControl = 24;
+constexpr int kRegsRows = 72, kRegsSplit = 56, kRegsState = 104, kRegsControl = 40;
 static_assert(2 * kRegsRows + 2 * kRegsSplit + 2 * kRegsState + kRegsControl <= 7 * kRegsLaunch &&
               4 * kRegsSplit + 2 * kRegsState + kRegsControl <= 7 * kRegsLaunch, "what a launch holds");
 constexpr uint32_t kTile = 32768, kAtom = 16384;  // 128 rows x 128 bf16: two swizzled atoms of 64 columns
 
+// A work item as the scheduling warp hands it out, in one of two slots with its head's tables.
+struct Item {
+  int n_chunks;  // -1: no more work
+  int t_begin, n_last, h;
+  float g;
+  int dst, to_local;  // where the state behind the item goes: index of a state in S_out or in `local`; -1: nowhere
+  int pad;
+  const float* S_in;  // entering state, or null (zero)
+};
+
 // Shared memory: with outputs two stages of [Q | K | V] and the bf16 state (K-major); state only three
 // stages of [K | V].  The state's tile (there: a spare one) also stages entering and final states.
+// Everything up to CF needs 1024-byte alignment, which the start of dynamic shared memory has here.
 template <bool OUT>
 struct Lay {
   static constexpr int kStages = OUT ? 2 : 3;
   static constexpr uint32_t Q = 0, K = OUT ? 2 * kTile : 0, V = K + kStages * kTile;
   static constexpr uint32_t S = V + kStages * kTile;
-  static constexpr uint32_t CF = S + kTile;        // pw(31 - j)
-  static constexpr uint32_t W = CF + 4 * 32;       // weight terms, of a whole and of the last chunk
-  static constexpr uint32_t BARS = W + 2 * 768;
-  static constexpr uint32_t SCRATCH = BARS + 8 * 40;
+  static constexpr uint32_t CF = S + kTile;      // per slot: pw(31 - j), 32 floats
+  static constexpr uint32_t W = CF + 2 * 128;    // per slot: weight terms, 192 words
+  static constexpr uint32_t ITEM = W + 2 * 768;  // per slot: the item
+  static constexpr uint32_t BARS = ITEM + 2 * 64;
+  static constexpr uint32_t STEAL = BARS + 8 * 48;
+  static constexpr uint32_t SCRATCH = STEAL + 16;
   static constexpr uint32_t TOTAL = SCRATCH + 4 * 16;
-  static constexpr uint32_t ALLOC = TOTAL + 1024;
-  static_assert(ALLOC <= 232448, "shared memory");
+  static_assert(sizeof(Item) <= 64 && TOTAL <= 232448, "shared memory");
 };
 // TMEM columns.  With outputs: QK (then P), O, KV, two A buffers; state only: two KV, four A buffers
 // ([h | r | m | l] of 32 tokens, 16 columns each).
@@ -88,116 +104,149 @@ struct Tmem {
   static_assert(cA + kABufs * ASTEP <= 512, "TMEM");
 };
 
-enum Bar { kFull = 0, kEmpty = 3, kAFull = 6, kAFree = 10, kKV = 14, kKVFree = 16, kQK = 18, kP, kOFull, kOFree, kStaged,
-           kSFull, kSFree, kFix, kDrainA, kDrainB, kCorner, kPair /* one per quad */, kBars = kPair + 4 };
+enum Bar { kFull = 0, kEmpty = 3, kAFull = 6, kAFree = 10, kKV = 14, kKVFree = 16, kQK = 18, kP, kOFull, kOFree,
+           kSFull, kSFree, kVRead, kStaged = kVRead + 2, kFix = kStaged + 2, kDrainA = kFix + 2, kDrainB, kCorner, kSteal, kItem, kItemFree = kItem + 2,
+           kPair = kItemFree + 2 /* one per quad */, kBars = kPair + 4 };
+static_assert(kBars <= 48, "barrier area");
+
+// One entry of the plan: a segment of a sequence.  seq < 0: none.
+struct Segment {
+  int seq, seg, n_seg, t_begin, len, local, pad0, pad1;
+};
+// The entering states of a cut sequence's segments are found sequence by sequence.
+struct CutSeq {
+  int seq, n_seg, local, last_len;
+};
 
 struct TcParams {
   const float* log_decay;
   const int32_t* cu;
   const float* S0;
-  float* local;  // [units][h_v][d_v][d_k]: the segments' own, then entering states
+  float* local;  // [cut segments][h_v][d_v][d_k]: the segments' own, then entering states
+  const Segment* list;  // the launch's items, or null: one sequence, segments in order
+  const CutSeq* cuts;   // linear_carry_kernel: cut sequences, or null: one sequence
   __nv_bfloat16* O;
   float* S_out;
   int* status;
   int n_seqs, total_tokens, h_k, h_v, d_k, d_v;
   int seg_tokens;  // INT_MAX: sequences are not cut
-  int skip_last;   // segment states only: the last segment of each sequence is not needed
+  int local_only;  // the segments' own states for a launch with outputs: the last one is not needed
   float scale;
 };
 
-// The work list: unit u is segment `seg` of sequence `seq`; sequences in order, those with a
-// malformed range (see chunk_info_n) left out, an empty sequence one unit.
-struct Unit {
-  int seq, seg, n_seg, t_begin, t_end, seq_end, first;
-  bool any_bad;
-};
 __device__ __forceinline__ int segments_of(int len, int seg_tokens) {
   return len <= seg_tokens ? 1 : (len - 1) / seg_tokens + 1;
 }
-
-// The unit `want`, or (want < 0) sequence `want_seq`'s units; seq = -1 when there is none.  The first
-// warp walks the offsets, 128 at a time with the next ones under way, and stops at the unit found
-// (`all`: goes on to the end, so that any_bad speaks of every range).  scratch: 8 ints.
-__device__ inline Unit find_unit(const int32_t* cu, int n_seqs, int total, int seg_tokens, int want, int want_seq, bool all,
-                                 int* scratch) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < 32) {
-    if (lane < 8) scratch[lane] = lane == 0 ? -1 : 0;
-    __syncwarp();
-    int carry = 0, high = INT_MIN, next[5];
-    bool found = false, bad = false;
-    auto fetch = [&](int base) {
-#pragma unroll
-      for (int e = 0; e < 5; ++e) next[e] = base + 4 * lane + e <= n_seqs ? cu[base + 4 * lane + e] : 0;
-    };
-    fetch(0);
-    for (int base = 0; base < n_seqs && (all || !found); base += 128) {
-      int off[5];
-#pragma unroll
-      for (int e = 0; e < 5; ++e) off[e] = next[e];
-      fetch(base + 128);
-      // the largest offset before each range: this lane's, the lanes' before it, the rounds' before
-      int top = INT_MIN;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (base + 4 * lane + e < n_seqs) top = max(top, max(off[e], off[e + 1]));
-      int incl = top;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl = max(incl, x);
-      }
-      int before = __shfl_up_sync(0xffffffffu, incl, 1);
-      before = lane == 0 ? high : max(high, before);
-      high = max(high, __shfl_sync(0xffffffffu, incl, 31));
-      int cnt[4], sum = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = base + 4 * lane + e < n_seqs;
-        const bool ok = in && off[e] >= 0 && off[e] >= before && off[e + 1] >= off[e] && off[e + 1] <= total;
-        if (in) before = max(before, max(off[e], off[e + 1]));
-        bad |= in && !ok;
-        cnt[e] = ok ? segments_of(off[e + 1] - off[e], seg_tokens) : 0;
-        sum += cnt[e];
-      }
-      int inc = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      int first = carry + inc - sum;
-      bool here = false;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = base + 4 * lane + e;
-        if (cnt[e] > 0 && (want >= 0 ? want >= first && want < first + cnt[e] : i == want_seq)) {
-          here = true;
-          scratch[0] = i;
-          scratch[1] = want >= 0 ? want - first : 0;
-          scratch[2] = cnt[e];
-          scratch[3] = off[e];
-          scratch[4] = off[e + 1];
-          scratch[5] = first;
-        }
-        first += cnt[e];
-      }
-      found |= __any_sync(0xffffffffu, here);
-      carry += __shfl_sync(0xffffffffu, inc, 31);
+// Segment `u` of a call with one sequence (seq = -1: there is no such segment).
+__device__ __forceinline__ Segment only_segment(const TcParams& p, int u) {
+  Segment s = {};
+  const int a = p.cu[0], b = p.cu[1];
+  s.seq = -1;
+  if (a >= 0 && b >= a && b <= p.total_tokens) {
+    s.n_seg = segments_of(b - a, p.seg_tokens);
+    if (u < s.n_seg) {
+      s.seq = 0;
+      s.seg = s.local = u;
+      s.t_begin = a + u * (s.n_seg > 1 ? p.seg_tokens : 0);
+      s.len = min(p.seg_tokens, b - s.t_begin);
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) scratch[6] = 1;
+  }
+  return s;
+}
+
+// The plan of a call with several sequences, one CTA: `units` entries, the segments of every sequence
+// with a valid range (longest first while they are at most kSortMost, else in order), then -1; `cut`
+// entries of the segments of cut sequences alone; `cuts` entries of the cut sequences.  A range
+// [cu[i], cu[i+1]) counts when 0 <= cu[i] <= cu[i+1] <= total_tokens and no earlier offset is above
+// cu[i]; others are reported.  An empty sequence is one segment of no tokens.
+constexpr int kPlanNT = 1024, kSortMost = 1024;
+__global__ void __launch_bounds__(kPlanNT) linear_plan_kernel(const int32_t* cu, int n_seqs, int total, int seg_tokens,
+                                                              Segment* list, int units, Segment* cut_list, int cut_units,
+                                                              CutSeq* cuts, int n_cuts, int* status) {
+  __shared__ int w_max[32], w_units[32], w_cut[32], w_cuts[32];
+  __shared__ int key[kSortMost];
+  grid_dep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < units; i += kPlanNT) list[i].seq = -1;
+  for (int i = tid; i < cut_units; i += kPlanNT) cut_list[i].seq = -1;
+  for (int i = tid; i < n_cuts; i += kPlanNT) cuts[i].seq = -1;
+  const bool sort = units <= kSortMost;
+  if (sort)
+    for (int i = tid; i < units; i += kPlanNT) key[i] = -1;
+  int c_max = INT_MIN, c_units = 0, c_cut = 0, c_cuts = 0;
+  __syncthreads();
+  for (int base = 0; base < n_seqs; base += kPlanNT) {
+    const int i = base + tid;
+    int a = 0, b = INT_MIN, top = INT_MIN;
+    if (i < n_seqs) {
+      a = cu[i];
+      b = cu[i + 1];
+      top = max(a, b);
+    }
+    int incl = top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = max(incl, x);
+    }
+    int before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) before = INT_MIN;
+    if (lane == 31) w_max[warp] = incl;
+    __syncthreads();
+    int all = c_max;
+    before = max(before, c_max);
+    for (int w = 0; w < kPlanNT / 32; ++w) {
+      if (w < warp) before = max(before, w_max[w]);
+      all = max(all, w_max[w]);
+    }
+    const bool ok = i < n_seqs && a >= 0 && a >= before && b >= a && b <= total;
+    if (i < n_seqs && !ok) atomicExch(status, GDN_ERR_SHAPE);
+    const int n = ok ? segments_of(b - a, seg_tokens) : 0;
+    // inclusive sums of segments, segments of cut sequences, cut sequences
+    int su = n, sc = n > 1 ? n : 0, sq = n > 1 ? 1 : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int xu = __shfl_up_sync(0xffffffffu, su, o), xc = __shfl_up_sync(0xffffffffu, sc, o),
+                xq = __shfl_up_sync(0xffffffffu, sq, o);
+      if (lane >= o) { su += xu; sc += xc; sq += xq; }
+    }
+    if (lane == 31) { w_units[warp] = su; w_cut[warp] = sc; w_cuts[warp] = sq; }
+    __syncthreads();
+    int bu = c_units, bc = c_cut, bq = c_cuts;
+    for (int w = 0; w < kPlanNT / 32; ++w) {
+      if (w < warp) { bu += w_units[w]; bc += w_cut[w]; bq += w_cuts[w]; }
+      c_units += w_units[w];
+      c_cut += w_cut[w];
+      c_cuts += w_cuts[w];
+    }
+    c_max = all;
+    bu += su - n;
+    bc += sc - (n > 1 ? n : 0);
+    bq += sq - (n > 1 ? 1 : 0);
+    for (int j = 0; j < n; ++j) {
+      Segment s = {};
+      s.seq = i; s.seg = j; s.n_seg = n; s.t_begin = a + j * (n > 1 ? seg_tokens : 0);
+      s.len = min(seg_tokens, b - s.t_begin); s.local = n > 1 ? bc + j : 0;
+      if (bu + j < units) {
+        list[bu + j] = s;
+        if (sort) key[bu + j] = s.len;
+      }
+      if (n > 1 && bc + j < cut_units) cut_list[bc + j] = s;
+    }
+    if (n > 1 && bq < n_cuts) cuts[bq] = CutSeq{i, n, bc, b - (a + (n - 1) * seg_tokens)};
+    __syncthreads();
+  }
+  if (!sort) return;
+  const int u = tid;
+  Segment s = {};
+  int rank = 0;
+  const bool have = u < units && key[u] >= 0;
+  if (have) {
+    s = list[u];
+    for (int j = 0; j < units; ++j) rank += key[j] > s.len || (key[j] == s.len && j < u);
   }
   __syncthreads();
-  Unit u;
-  u.seq = scratch[0];
-  u.seg = scratch[1];
-  u.n_seg = scratch[2];
-  u.seq_end = scratch[4];
-  u.first = scratch[5];
-  u.any_bad = scratch[6] != 0;
-  u.t_begin = scratch[3] + u.seg * (u.n_seg > 1 ? seg_tokens : 0);
-  u.t_end = u.seg + 1 < u.n_seg ? u.t_begin + seg_tokens : u.seq_end;
-  return u;
+  if (have) list[rank] = s;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -236,6 +285,26 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// Work stealing: asks for a block of this grid that has not been launched yet; its index, if there is
+// one, arrives in the 16 bytes at `resp`.
+__device__ __forceinline__ void steal_block(void* resp, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(resp)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ bool stolen_block(const void* resp, int& block) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(resp))
+      : "memory");
+  block = (int)x;
+  return got != 0;
+}
 // Four 8x8 bf16 tiles, transposed: register i of a thread holds two consecutive rows of tile i's
 // column lane / 4.
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
@@ -251,7 +320,8 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Packed bf16 products, rounded once.
+// Packed bf16 arithmetic, every result rounded once.
+constexpr uint32_t kNeg = 0x80008000u;  // flips both signs
 __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -272,6 +342,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// The weights lambda^back and lambda^(back - 1) of two consecutive tokens (0 at a negative exponent) as
+// three packed bf16 terms each, which sum to them exactly.
+__device__ __forceinline__ void weight_terms(int back, float g, uint32_t& a, uint32_t& b, uint32_t& c) {
+  uint32_t t[2][3];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int e = back - x;
+    float w = e < 0 ? 0.f : e == 0 ? 1.f : expf((float)e * g);
+#pragma unroll
+    for (int y = 0; y < 3; ++y) {
+      t[x][y] = __float_as_uint(w) & 0xffff0000u;
+      w -= __uint_as_float(t[x][y]);
+    }
+  }
+  a = t[0][0] >> 16 | t[1][0];
+  b = t[0][1] >> 16 | t[1][1];
+  c = t[0][2] >> 16 | t[1][2];
+}
 // Registers per thread of the calling warpgroup.
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -285,40 +373,32 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                : "memory");
 }
 
-// OUT: outputs and the final state; otherwise the states of the units alone (to S_out when a sequence
-// is one unit, to `local`, from zero, when it is cut).
+// OUT: outputs and the final state; otherwise the states of the items alone (to S_out when a sequence
+// is one segment, to `local`, from zero, when it is cut).
 template <bool OUT>
 __global__ void __launch_bounds__(NT, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
+                     const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_local,
                      const TcParams p) {
   using L = Lay<OUT>;
   using TM = Tmem<OUT>;
-  static_assert(kBars <= 40, "barrier area");
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* cf = reinterpret_cast<float*>(sm + L::CF);
-  uint32_t* wtab = reinterpret_cast<uint32_t*>(sm + L::W);
+  constexpr int kStages = L::kStages;
+  extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BARS);
   int* scratch = reinterpret_cast<int*>(sm + L::SCRATCH);
-  volatile int* dead = scratch + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 9);
-  int* issued = scratch + 10;  // chunks whose loads were issued
+  volatile int* dead = scratch;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 1);
+  int* issued = scratch + 2;  // chunks whose loads were issued
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2, quad = warp & 3;
-  const int h = blockIdx.x % p.h_v;
-  const int unit = blockIdx.x / p.h_v;
-  const Unit un = find_unit(p.cu, p.n_seqs, p.total_tokens, p.seg_tokens, unit, 0, unit == 0 && h == 0, scratch);
-  if (unit == 0 && h == 0 && tid == 0 && un.any_bad) atomicExch(p.status, GDN_ERR_SHAPE);
-  if (un.seq < 0) return;
-  if (!OUT && p.skip_last && un.seg + 1 == un.n_seg) return;  // (a sequence of one segment too)
-  const int t_begin = un.t_begin, len = un.t_end - un.t_begin;
-  const int n_chunks = (len + C - 1) / C;
-  const int n_last = len - (n_chunks - 1) * C;  // tokens of the last chunk
-  const int hk = h / (p.h_v / p.h_k);
   const int dkp = p.d_k <= 64 ? 64 : 128, dvp = p.d_v <= 64 ? 64 : 128;  // columns that the products cover
-  const float g = p.log_decay[h];
+  const size_t dd = (size_t)p.d_v * p.d_k;
 
+  if (smem_u32(sm) & 1023u) {  // (the swizzled tiles could not be addressed)
+    if (tid == 0) atomicExch(p.status, GDN_ERR_CUDA);
+    return;
+  }
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -327,8 +407,11 @@ __global__ void __launch_bounds__(NT, 1)
     for (int b = 0; b < kBars; ++b) {
       int count = 1;
       if (b >= kEmpty && b < kEmpty + 3) count = OUT ? 2 : 1;  // the issuing warps' commits
-      if (b >= kAFull && b < kAFull + 4) count = 4;             // the warps of a splitting group
-      if (b == kP || b == kOFree || b == kStaged || b == kSFull || b == kKVFree || b == kKVFree + 1 || b == kFix || b == kCorner) count = 8;
+      if (b >= kAFull && b < kAFull + 4) count = 4;            // the warps of a splitting group
+      if (b == kP || b == kOFree || b == kSFull || b == kKVFree || b == kKVFree + 1 ||
+          (b >= kVRead && b < kFix + 2) || b == kCorner)
+        count = 8;
+      if (b >= kItemFree && b < kItemFree + 2) count = OUT ? 27 : 26;  // every warp that reads items
       if (b >= kPair) count = 2;
       mbar_init(&bar[b], count);
     }
@@ -336,34 +419,13 @@ __global__ void __launch_bounds__(NT, 1)
     *dead = 0;
     *issued = 0;
   }
-  if (tid < 32) cf[tid] = tid == 31 ? 1.f : expf((float)(31 - tid) * g);
-  // Weight terms: word 12 (4 q + j) + 4 term + e holds those of tokens 32 q + 8 e + 2 j + {0, 1}; the
-  // second table those of the last chunk, zero behind its end.
-  if (tid >= 64 && tid < 64 + 128) {
-    const int i = tid - 64, which = i >> 6, q = (i >> 4) & 3, j = (i >> 2) & 3, e = i & 3;
-    const int n = which ? n_last : C;
-    uint32_t term[3] = {0u, 0u, 0u};
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int back = n - 1 - (32 * q + 8 * e + 2 * j + x);
-      float w = back < 0 ? 0.f : back == 0 ? 1.f : expf((float)back * g);
-#pragma unroll
-      for (int y = 0; y < 3; ++y) {
-        const uint32_t b = __float_as_uint(w) & 0xffff0000u;
-        w -= __uint_as_float(b);
-        term[y] |= x ? b : b >> 16;
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < 3; ++y) wtab[192 * which + 12 * (4 * q + j) + 4 * y + e] = term[y];
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
-  auto wait = [&](int b, int parity) {
-    if (mbar_wait(&bar[b], (uint32_t)(parity & 1), kWaitNs)) return true;
+  auto wait = [&](int b, int parity, uint64_t limit = kWaitNs) {
+    if (mbar_wait(&bar[b], (uint32_t)(parity & 1), limit)) return true;
     *dead = 1;
     return false;
   };
@@ -371,106 +433,145 @@ __global__ void __launch_bounds__(NT, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[b]);
   };
+  auto item_at = [&](int k) { return reinterpret_cast<const Item*>(sm + L::ITEM + 64 * (k & 1)); };
+  // Item k is there (n_chunks < 0: the work is done).  (A whole item may pass meanwhile.)
+  constexpr uint64_t kItemNs = 8 * kWaitNs;
+  auto get_item = [&](int k) { return wait(kItem + (k & 1), k >> 1, kItemNs) && item_at(k)->n_chunks >= 0; };
+  auto release_item = [&](int k) { arrive(kItemFree + (k & 1)); };
+  // Every role counts the chunks of all its items, gc: stages, accumulators and phases go by that.  A
+  // barrier's next phase but one never completes before every waiter has seen this one: its arrivals
+  // follow, through other barriers, from what the waiter does next.  (Two each, by turns: kVRead, since
+  // the splitting warps can be done with two chunks' values before the rows' warps look; kStaged, two
+  // chunks' outputs before the loading warp does; kFix, the ends of two one-chunk items before the warp
+  // that issues PV does.)
 
   if (OUT && group < 2) {
     // ------------------------------------------------------------ scores to P, outputs
     const int t = 32 * quad + lane;
-    const float rho = fmaxf(expf((float)(t + 1) * g), 8.673617379884035e-19f);  // 2^-60
-    const float inv = 1.f / rho, f = rho * p.scale;
-    // The factor of a score is lambda^(t - s) / rho_t = rf cf[j] for column j of a block: rf =
-    // lambda^(t - 32 b - 31) / rho_t, and cf[j] = lambda^(31 - j).  On the diagonal (t - 32 b = lane)
-    // rf's power has a negative exponent; where rf could leave the fp32 range (a decay below e^-1.4 per
-    // token) the block takes cf[31 - lane + j] instead.
-    const bool steep = !(cf[0] > 1e-19f);
-    float rf[2];
+    bool ok = true;
+    for (int k = 0, gc = 0; ok && get_item(k); ++k) {
+      const Item& it = *item_at(k);
+      const float* cf = reinterpret_cast<const float*>(sm + L::CF + 128 * (k & 1));
+      const int n_chunks = it.n_chunks, n_last = it.n_last, h = it.h, t_begin = it.t_begin;
+      const float g = it.g;
+      const float rho = fmaxf(expf((float)(t + 1) * g), 8.673617379884035e-19f);  // 2^-60
+      const float inv = 1.f / rho, f = rho * p.scale;
+      // The factor of a score is lambda^(t - s) / rho_t = rf cf[j] for column j of a block: rf =
+      // lambda^(t - 32 b - 31) / rho_t, and cf[j] = lambda^(31 - j).  On the diagonal (t - 32 b = lane)
+      // rf's power has a negative exponent; where rf could leave the fp32 range (a decay below e^-1.4
+      // per token) the block takes cf[31 - lane + j] instead.
+      const bool steep = !(cf[0] > 1e-19f);
+      // Where no rho_t of the chunk is held back, the factor is lambda^-(s + 1), the column's alone.
+      const bool gentle = expf((float)C * g) >= 8.673617379884035e-19f;
+      float rc[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int b = 2 * i + group;
-      rf[i] = b < quad ? expf((float)(t - 32 * b - 31) * g) * inv : steep ? inv : inv / cf[lane];
-    }
-    for (int c = 0; c < n_chunks; ++c) {
-      const int n = c + 1 < n_chunks ? C : n_last;
-      if (!wait(kQK, c)) break;
-      tc_fence_after();
-      // Blocks of 32 columns: the row's blocks before `quad` whole, its own up to the diagonal, none
-      // behind.  P overwrites scores that the other warp of this quad may still be reading, so both
-      // read and round first.
-      uint32_t o[2][16];
+      for (int i = 0; i < 2; ++i) rc[i] = gentle ? expf(-(float)(32 * (2 * i + group) + 32) * g) : 0.f;
+      float rf[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int b = 2 * i + group;
-        if (b <= quad) {
-          float x[32];
-          tmem_ld32(tmem + lane_base + TM::cP + 32 * b, x);
-          tmem_ld_wait();
-          if (b < quad || !steep) {
-            const uint64_t rf2 = pair(rf[i], rf[i]);
-            const int seen = b < quad ? 31 : lane;  // the last column that counts
+        rf[i] = b < quad ? expf((float)(t - 32 * b - 31) * g) * inv : steep ? inv : inv / cf[lane];
+      }
+      for (int c = 0; c < n_chunks; ++c, ++gc) {
+        const int n = c + 1 < n_chunks ? C : n_last;
+        if (!(ok = wait(kQK, gc))) break;
+        tc_fence_after();
+        // Blocks of 32 columns: the row's blocks before `quad` whole, its own up to the diagonal, none
+        // behind.  P overwrites scores that the other warp of this quad may still be reading, so both
+        // read and round first.
+        uint32_t o[2][16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cf + j);
-              float y0, y1, y2, y3;
-              unpair(mul2(pair(x[j], x[j + 1]), mul2(rf2, w.x)), y0, y1);
-              unpair(mul2(pair(x[j + 2], x[j + 3]), mul2(rf2, w.y)), y2, y3);
-              o[i][j / 2] = pack_bf16(j <= seen ? y0 : 0.f, j + 1 <= seen ? y1 : 0.f);
-              o[i][j / 2 + 1] = pack_bf16(j + 2 <= seen ? y2 : 0.f, j + 3 <= seen ? y3 : 0.f);
+        for (int i = 0; i < 2; ++i) {
+          const int b = 2 * i + group;
+          if (b <= quad) {
+            float x[32];
+            tmem_ld32(tmem + lane_base + TM::cP + 32 * b, x);
+            tmem_ld_wait();
+            if (gentle) {
+              const uint64_t rf2 = pair(rc[i], rc[i]);
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cf + j);
+                float y0, y1, y2, y3;
+                unpair(mul2(pair(x[j], x[j + 1]), mul2(rf2, w.x)), y0, y1);
+                unpair(mul2(pair(x[j + 2], x[j + 3]), mul2(rf2, w.y)), y2, y3);
+                o[i][j / 2] = pack_bf16(y0, y1);
+                o[i][j / 2 + 1] = pack_bf16(y2, y3);
+              }
+              if (b == quad) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) o[i][j / 2] &= lane > j ? 0xffffffffu : lane == j ? 0xffffu : 0u;
+              }
+            } else if (b < quad || !steep) {
+              const uint64_t rf2 = pair(rf[i], rf[i]);
+              const int seen = b < quad ? 31 : lane;  // the last column that counts
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cf + j);
+                float y0, y1, y2, y3;
+                unpair(mul2(pair(x[j], x[j + 1]), mul2(rf2, w.x)), y0, y1);
+                unpair(mul2(pair(x[j + 2], x[j + 3]), mul2(rf2, w.y)), y2, y3);
+                o[i][j / 2] = pack_bf16(j <= seen ? y0 : 0.f, j + 1 <= seen ? y1 : 0.f);
+                o[i][j / 2 + 1] = pack_bf16(j + 2 <= seen ? y2 : 0.f, j + 3 <= seen ? y3 : 0.f);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float y0 = j <= lane ? x[j] * (cf[31 - lane + j] * rf[i]) : 0.f;
+                const float y1 = j + 1 <= lane ? x[j + 1] * (cf[32 - lane + j] * rf[i]) : 0.f;
+                o[i][j / 2] = pack_bf16(y0, y1);
+              }
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float y0 = j <= lane ? x[j] * (cf[31 - lane + j] * rf[i]) : 0.f;
-              const float y1 = j + 1 <= lane ? x[j + 1] * (cf[32 - lane + j] * rf[i]) : 0.f;
-              o[i][j / 2] = pack_bf16(y0, y1);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[i][j] = 0u;
-        }
-      }
-      arrive(kPair + quad);
-      if (!wait(kPair + quad, c)) break;
-      tmem_st16(tmem + lane_base + TM::cP + 16 * group, o[0]);
-      tmem_st16(tmem + lane_base + TM::cP + 32 + 16 * group, o[1]);
-      tmem_st_wait();
-      tc_fence_before();
-      arrive(kP);
-      if (!wait(kOFull, c)) break;
-      tc_fence_after();
-      // The outputs, rounded, into the stage of Q (whose readers are done)
-      unsigned char* stage = sm + L::Q + (c & 1) * kTile;
-      if (64 * group < dvp) {
-        const uint64_t f2 = pair(f, f);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float x[32];
-          tmem_ld32(tmem + lane_base + TM::cO + 64 * group + 32 * b, x);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float y0, y1;
-              unpair(mul2(f2, pair(x[j + 2 * e], x[j + 2 * e + 1])), y0, y1);
-              y[e] = pack_bf16(y0, y1);
-            }
-            *reinterpret_cast<uint4*>(stage + kbf16(t, 64 * group + 32 * b + j, 128)) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int j = 0; j < 16; ++j) o[i][j] = 0u;
           }
         }
-      }
-      tc_fence_before();
-      arrive(kOFree);
-      if (n == C) {
+        arrive(kPair + quad);
+        if (!(ok = wait(kPair + quad, gc))) break;
+        tmem_st16(tmem + lane_base + TM::cP + 16 * group, o[0]);
+        tmem_st16(tmem + lane_base + TM::cP + 32 + 16 * group, o[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        arrive(kP);
+        if (!(ok = wait(kOFull, gc))) break;
+        tc_fence_after();
+        // The outputs, rounded, into the stage of V, once the splitting warps have read it too
+        if (!(ok = wait(kVRead + (gc & 1), gc >> 1))) break;
+        unsigned char* stage = sm + L::V + (gc & 1) * kTile;
+        if (64 * group < dvp) {
+          const uint64_t f2 = pair(f, f);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float x[32];
+            tmem_ld32(tmem + lane_base + TM::cO + 64 * group + 32 * b, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float y0, y1;
+                unpair(mul2(f2, pair(x[j + 2 * e], x[j + 2 * e + 1])), y0, y1);
+                y[e] = pack_bf16(y0, y1);
+              }
+              *reinterpret_cast<uint4*>(stage + kbf16(t, 64 * group + 32 * b + j, 128)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        arrive(kOFree);
+        // (of a part of a chunk the rows behind its end are not this sequence's: row by row)
+        if (n < C && 8 * (lane & 7) + 64 * group < p.d_v) {
+          const int col = 64 * group + 8 * (lane & 7);
+          for (int row = 32 * quad + (lane >> 3); row < min(n, 32 * quad + 32); row += 4)
+            *reinterpret_cast<uint4*>(p.O + ((size_t)(t_begin + c * C + row) * p.h_v + h) * p.d_v + col) =
+                *reinterpret_cast<const uint4*>(stage + kbf16(row, col, 128));
+        }
         fence_async_smem();
-        arrive(kStaged);
-      } else if (8 * (lane & 7) + 64 * group < p.d_v) {
-        // a part of a chunk: the rows behind its end are not this sequence's
-        const int col = 64 * group + 8 * (lane & 7);
-        for (int row = 32 * quad + (lane >> 3); row < min(n, 32 * quad + 32); row += 4)
-          *reinterpret_cast<uint4*>(p.O + ((size_t)(t_begin + c * C + row) * p.h_v + h) * p.d_v + col) =
-              *reinterpret_cast<const uint4*>(stage + kbf16(row, col, 128));
+        arrive(kStaged + (gc & 1));
       }
+      release_item(k);
     }
   } else if (group < 4) {
     // ------------------------------------------------------------ values to A operands
@@ -482,59 +583,68 @@ __global__ void __launch_bounds__(NT, 1)
     const int lm_tok = (lane & 7) + 8 * (lane >> 4), lm_d = 32 * quad + 8 * ((lane >> 3) & 1);
     const uint32_t at = tmem + lane_base + TM::cA + buf * TM::ASTEP;
     bool ok = true;
-    for (int c = 0; c < n_chunks && ok; ++c) {
-      const int st = c % L::kStages, n = c + 1 < n_chunks ? C : n_last;
-      if (!(ok = wait(kFull + st, c / L::kStages))) break;
-      const uint32_t* table = wtab + (n == C ? 0 : 192) + 12 * (lane & 3);
+    for (int k = 0, gc = 0; ok && get_item(k); ++k) {
+      const int n_chunks = item_at(k)->n_chunks, n_last = item_at(k)->n_last;
+      const uint32_t* table = reinterpret_cast<const uint32_t*>(sm + L::W + 768 * (k & 1)) + 12 * (lane & 3);
+      for (int c = 0; c < n_chunks && ok; ++c, ++gc) {
+        const int st = gc % kStages, n = c + 1 < n_chunks ? C : n_last;
+        if (!(ok = wait(kFull + st, gc / kStages))) break;
 #pragma unroll 1
-      for (int i = 0; i < kPer; ++i) {
-        const int q = buf + TM::kABufs * i, m = c * kPer + i;
-        uint32_t x[4][4];  // tiles of 16 rows x 16 tokens: (rows +0, tokens +0), (+0, +16), (+16, +0), (+16, +16)
-        uint32_t wt[3][4];
-        if (rows) {
-          const uint32_t vt = smem_u32(sm + L::V + st * kTile) + (uint32_t)(32 * q + lm_tok) * 128u;
+        for (int i = 0; i < kPer; ++i) {
+          const int q = buf + TM::kABufs * i, m = gc * kPer + i;
+          uint32_t x[4][4];  // tiles of 16 rows x 16 tokens: (rows +0, tokens +0), (+0, +16), (+16, +0), (+16, +16)
+          uint32_t wt[3][4];
+          if (rows) {
+            const uint32_t vt = smem_u32(sm + L::V + st * kTile) + (uint32_t)(32 * q + lm_tok) * 128u;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int d = lm_d + 16 * (b >> 1);
-            ldmatrix_x4_trans(vt + (d >> 6) * kAtom + 2048 * (b & 1) + ((((d & 63) >> 3) ^ (lm_tok & 7)) << 4), x[b]);
-          }
-#pragma unroll
-          for (int y = 0; y < 3; ++y) {
-            const uint4 u = *reinterpret_cast<const uint4*>(table + 48 * q + 4 * y);
-            wt[y][0] = u.x; wt[y][1] = u.y; wt[y][2] = u.z; wt[y][3] = u.w;
-          }
-          if (n < C) {  // (a row behind the last token may hold anything)
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int tok = 32 * q + 16 * (b & 1) + 8 * (j >> 1) + 2 * (lane & 3);
-                x[b][j] = tok >= n ? 0u : tok + 1 >= n ? x[b][j] & 0xffffu : x[b][j];
-              }
-          }
-        }
-        if (m > 0 && !(ok = wait(kAFree + buf, m - 1))) break;
-        tc_fence_after();
-        if (rows) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t t[4][8];  // h, r, m, l of 16 rows x 32 tokens
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t v = x[2 * half + (j >> 2)][j & 3], *w = &wt[0][j >> 1];
-              t[0][j] = bmul2(v, w[0]);
-              t[1][j] = bfma2(v, w[0], t[0][j] ^ 0x80008000u);
-              t[2][j] = bmul2(v, w[4]);
-              t[3][j] = bfma2(v, w[8], bfma2(v, w[4], t[2][j] ^ 0x80008000u));
+            for (int b = 0; b < 4; ++b) {
+              const int d = lm_d + 16 * (b >> 1);
+              ldmatrix_x4_trans(vt + (d >> 6) * kAtom + 2048 * (b & 1) + ((((d & 63) >> 3) ^ (lm_tok & 7)) << 4), x[b]);
             }
+            if (n == C) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) tmem_st_16x128b_x4(at + ((uint32_t)(16 * half) << 16) + 16 * y, t[y]);
+              for (int y = 0; y < 3; ++y) {
+                const uint4 u = *reinterpret_cast<const uint4*>(table + 48 * q + 4 * y);
+                wt[y][0] = u.x; wt[y][1] = u.y; wt[y][2] = u.z; wt[y][3] = u.w;
+              }
+            } else {  // the weights count back from the last token; a row behind it may hold anything
+              const float g = item_at(k)->g;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) weight_terms(n - 1 - (32 * q + 8 * e + 2 * (lane & 3)), g, wt[0][e], wt[1][e], wt[2][e]);
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int tok = 32 * q + 16 * (b & 1) + 8 * (j >> 1) + 2 * (lane & 3);
+                  x[b][j] = tok >= n ? 0u : tok + 1 >= n ? x[b][j] & 0xffffu : x[b][j];
+                }
+            }
           }
-          tmem_st_wait();
+          if (OUT && i + 1 == kPer) arrive(kVRead + (gc & 1));
+          if (m > 0 && !(ok = wait(kAFree + buf, m - 1))) break;
+          tc_fence_after();
+          if (rows) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t t[4][8];  // h, r, m, l of 16 rows x 32 tokens
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t v = x[2 * half + (j >> 2)][j & 3], *w = &wt[0][j >> 1];
+                t[0][j] = bmul2(v, w[0]);
+                t[1][j] = bfma2(v, w[0], t[0][j] ^ kNeg);
+                t[2][j] = bmul2(v, w[4]);
+                t[3][j] = bfma2(v, w[8], bfma2(v, w[4], t[2][j] ^ kNeg));
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y) tmem_st_16x128b_x4(at + ((uint32_t)(16 * half) << 16) + 16 * y, t[y]);
+            }
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          arrive(kAFull + buf);
         }
-        tc_fence_before();
-        arrive(kAFull + buf);
       }
+      release_item(k);
     }
   } else if (group < 6) {
     // ------------------------------------------------------------ the state
@@ -542,39 +652,12 @@ __global__ void __launch_bounds__(NT, 1)
     const int hw = group - 4;
     const int r = 32 * quad + lane;  // row of S
     const bool mine = 32 * quad < dvp && 64 * hw < dkp;
-    float s[64];
-    const float* S_in = nullptr;
-    if (un.n_seg == 1) {
-      if (p.S0) S_in = p.S0 + ((size_t)un.seq * p.h_v + h) * p.d_v * p.d_k;
-    } else if (OUT) {
-      S_in = p.local + ((size_t)unit * p.h_v + h) * p.d_v * p.d_k;
-    }
     // Entering and final states pass through a corner of the state's tile, 32 rows x 32 columns per warp
-    // (16-byte chunks swizzled by row), so that global memory sees whole 128-byte lines.
+    // (16-byte chunks swizzled by row, as a tensor copy with 128-byte swizzle has them), so that global
+    // memory sees whole 128-byte lines.
     float* corner = reinterpret_cast<float*>(sm + L::S) + 1024 * (warp - 16);
     const int my_chunk = lane & 7, my_row = lane >> 3;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int k = 64 * hw + 32 * j + 4 * my_chunk;
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = 4 * i + my_row;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (S_in && 32 * quad + row < p.d_v && k < p.d_k)
-          x = *reinterpret_cast<const float4*>(S_in + (size_t)(32 * quad + row) * p.d_k + k);
-        *reinterpret_cast<float4*>(corner + 32 * row + 4 * (my_chunk ^ (row & 7))) = x;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 x = *reinterpret_cast<const float4*>(corner + 32 * lane + 4 * (i ^ (lane & 7)));
-        s[32 * j + 4 * i] = x.x; s[32 * j + 4 * i + 1] = x.y; s[32 * j + 4 * i + 2] = x.z; s[32 * j + 4 * i + 3] = x.w;
-      }
-    }
-    // (the rounded state that follows is written over other warps' corners)
-    arrive(kCorner);
-    if (!wait(kCorner, 0)) s[0] = 0.f;
+    float s[64];
     auto publish_state = [&]() {  // the state, rounded to bf16, as QS's B operand
       if (mine) {
 #pragma unroll
@@ -586,76 +669,115 @@ __global__ void __launch_bounds__(NT, 1)
       fence_async_smem();
       arrive(kSFull);
     };
-    if (OUT && n_chunks > 0) publish_state();
-    const DecayStep step = decay_step(g, C);
     bool ok = true;
-    for (int c = 0; c < n_chunks && ok; ++c) {
-      const int st = c % L::kStages, kv = c % TM::kKVBufs, n = c + 1 < n_chunks ? C : n_last;
-      if (n < C) {
-        // rows behind the last token: another sequence's, or none; they may hold anything
-        if (!(ok = wait(kFull + st, c / L::kStages))) break;
-        const int per_row = (dkp + dvp) / 8;
-        for (int e = tid - 512; e < (C - n) * per_row; e += 256) {
-          const int row = n + e / per_row, x = e % per_row;
-          unsigned char* tile = x < dkp / 8 ? sm + L::K + st * kTile : sm + L::V + st * kTile;
-          const int col = x < dkp / 8 ? x : x - dkp / 8;
-          *reinterpret_cast<uint4*>(tile + (col >> 3) * kAtom + row * 128 + (col & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0, gc = 0, fixes = 0; ok && get_item(k); ++k) {
+      const int n_chunks = item_at(k)->n_chunks, n_last = item_at(k)->n_last;
+      if (const float* S_in = item_at(k)->S_in) {
+        // (all loads under way at once: s holds them in the order of memory first)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = 4 * (i & 7) + my_row, col = 64 * hw + 32 * (i >> 3) + 4 * my_chunk;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (32 * quad + row < p.d_v && col < p.d_k)
+            x = *reinterpret_cast<const float4*>(S_in + (size_t)(32 * quad + row) * p.d_k + col);
+          s[4 * i] = x.x; s[4 * i + 1] = x.y; s[4 * i + 2] = x.z; s[4 * i + 3] = x.w;
         }
-        fence_async_smem();
-        arrive(kFix);
+        bulk_wait_read_all();  // (the final state before this one has left the corner)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + my_row;
+            *reinterpret_cast<float4*>(corner + 32 * row + 4 * (my_chunk ^ (row & 7))) =
+                make_float4(s[32 * j + 4 * i], s[32 * j + 4 * i + 1], s[32 * j + 4 * i + 2], s[32 * j + 4 * i + 3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(corner + 32 * lane + 4 * (i ^ (lane & 7)));
+            s[32 * j + 4 * i] = x.x; s[32 * j + 4 * i + 1] = x.y; s[32 * j + 4 * i + 2] = x.z; s[32 * j + 4 * i + 3] = x.w;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) s[j] = 0.f;
+        bulk_wait_read_all();
       }
-      if (!(ok = wait(kKV + kv, c / TM::kKVBufs))) break;
-      tc_fence_after();
-      const DecayStep f = n == C ? step : decay_step(g, n);
-      if (mine) {
-        const uint32_t at = tmem + lane_base + TM::cKV + 128 * kv + 64 * hw;
-        const uint64_t m = f.near1 ? pair(f.f1, f.f1) : pair(f.f, f.f);
+      if (OUT) {  // (the rounded state is written over other warps' corners)
+        arrive(kCorner);
+        if (!(ok = wait(kCorner, k))) break;
+        if (n_chunks > 0) publish_state();
+      }
+      for (int c = 0; c < n_chunks; ++c, ++gc) {
+        const int st = gc % kStages, kv = gc % TM::kKVBufs, n = c + 1 < n_chunks ? C : n_last;
+        if (n < C) {
+          // rows behind the last token: another sequence's, or none; they may hold anything
+          if (!(ok = wait(kFull + st, gc / kStages))) break;
+          const int per_row = (dkp + dvp) / 8;
+          for (int e = tid - 512; e < (C - n) * per_row; e += 256) {
+            const int row = n + e / per_row, x = e % per_row;
+            unsigned char* tile = x < dkp / 8 ? sm + L::K + st * kTile : sm + L::V + st * kTile;
+            const int col = x < dkp / 8 ? x : x - dkp / 8;
+            *reinterpret_cast<uint4*>(tile + (col >> 3) * kAtom + row * 128 + (col & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+          arrive(kFix + (fixes & 1));
+          ++fixes;
+        }
+        if (!(ok = wait(kKV + kv, gc / TM::kKVBufs))) break;
+        tc_fence_after();
+        if (mine) {
+          const DecayStep f = decay_step(item_at(k)->g, n);
+          const uint32_t at = tmem + lane_base + TM::cKV + 128 * kv + 64 * hw;
+          const uint64_t m = f.near1 ? pair(f.f1, f.f1) : pair(f.f, f.f);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float x[32];
-          tmem_ld32(at + 32 * b, x);
-          tmem_ld_wait();
+          for (int b = 0; b < 4; ++b) {
+            float x[16];
+            tmem_ld16(at + 16 * b, x);
+            tmem_ld_wait();
+            if (f.near1) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float &s0 = s[32 * b + j], &s1 = s[32 * b + j + 1];
-            const uint64_t d = pair(x[j], x[j + 1]), a = pair(s0, s1);
-            unpair(fma2(a, m, f.near1 ? add2(a, d) : d), s0, s1);
+              for (int j = 0; j < 16; j += 2) {
+                const uint64_t a = pair(s[16 * b + j], s[16 * b + j + 1]);
+                unpair(fma2(a, m, add2(a, pair(x[j], x[j + 1]))), s[16 * b + j], s[16 * b + j + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j += 2)
+                unpair(fma2(pair(s[16 * b + j], s[16 * b + j + 1]), m, pair(x[j], x[j + 1])), s[16 * b + j], s[16 * b + j + 1]);
+            }
+          }
+        }
+        tc_fence_before();
+        arrive(kKVFree + kv);
+        if (OUT) {  // (the tile's readers are done: it takes the next rounding, or the final state's corners)
+          if (!(ok = wait(kSFree, gc))) break;
+          if (c + 1 < n_chunks) publish_state();
+        }
+      }
+      if (!ok) break;
+      if (item_at(k)->dst >= 0 && mine) {
+        const CUtensorMap* map = item_at(k)->to_local ? &map_local : &map_s;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (j) bulk_wait_read_all();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(corner + 32 * lane + 4 * (i ^ (lane & 7))) =
+                make_float4(s[32 * j + 4 * i], s[32 * j + 4 * i + 1], s[32 * j + 4 * i + 2], s[32 * j + 4 * i + 3]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(map, corner, 64 * hw + 32 * j, 32 * quad, item_at(k)->dst);
+            bulk_commit();
           }
         }
       }
-      tc_fence_before();
-      arrive(kKVFree + kv);
-      if (OUT && c + 1 < n_chunks) {
-        if (!(ok = wait(kSFree, c))) break;
-        publish_state();
-      }
+      release_item(k);
     }
-    float* dst = nullptr;
-    if (un.n_seg == 1 || (OUT && un.seg + 1 == un.n_seg))
-      dst = p.S_out + ((size_t)un.seq * p.h_v + h) * p.d_v * p.d_k;
-    else if (!OUT)
-      dst = p.local + ((size_t)unit * p.h_v + h) * p.d_v * p.d_k;
-    // (the last reader of the state's tile, QS of the last chunk, must be done with it)
-    if (OUT && ok && n_chunks > 0) ok = wait(kSFree, n_chunks - 1);
-    if (dst && ok) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = 64 * hw + 32 * j + 4 * my_chunk;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(corner + 32 * lane + 4 * (i ^ (lane & 7))) =
-              make_float4(s[32 * j + 4 * i], s[32 * j + 4 * i + 1], s[32 * j + 4 * i + 2], s[32 * j + 4 * i + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 4 * i + my_row;
-          if (32 * quad + row < p.d_v && k < p.d_k)
-            *reinterpret_cast<float4*>(dst + (size_t)(32 * quad + row) * p.d_k + k) =
-                *reinterpret_cast<const float4*>(corner + 32 * row + 4 * (my_chunk ^ (row & 7)));
-        }
-      }
-    }
+    bulk_wait_read_all();
   } else {
     regs_dec<kRegsControl>();
     if (quad == 0) {
@@ -664,54 +786,68 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t idQK = idesc_bf16(128, 128, false, false), idQS = idesc_bf16(128, dvp, false, false),
                        idPV = idesc_bf16(128, dvp, false, true);
         const int nk = (p.d_k + 15) / 16;
-        const uint64_t dS = sdesc_sw128(smem_u32(sm + L::S), 16, 1024);
-        auto issue_qk = [&](int c) {
-          if (!wait(kFull + (c & 1), c >> 1)) return false;
+        const uint64_t dQ0 = sdesc_sw128(smem_u32(sm + L::Q), 16, 1024), dK0 = sdesc_sw128(smem_u32(sm + L::K), 16, 1024),
+                       dS = sdesc_sw128(smem_u32(sm + L::S), 16, 1024), dV0 = sdesc_sw128(smem_u32(sm + L::V), kAtom, 1024);
+        int k = -1, left = 0, fixes = 0;  // item, its chunks not yet begun
+        bool ok = true;
+        // The next chunk's item, past items of no tokens; false when the work is done.
+        auto next_chunk = [&]() {
+          while (left == 0) {
+            if (k >= 0) release_item(k);
+            if (!get_item(++k)) return false;
+            left = item_at(k)->n_chunks;
+          }
+          --left;
+          return true;
+        };
+        auto issue_qk = [&](int gc) {
+          if (!wait(kFull + (gc & 1), gc >> 1)) return false;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::Q + (c & 1) * kTile), 16, 1024);
-            const uint64_t dK = sdesc_sw128(smem_u32(sm + L::K + (c & 1) * kTile), 16, 1024);
+            const uint64_t st = (uint64_t)((gc & 1) * kTile) >> 4;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < nk) {
-                const uint64_t off = (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4);
-                mma_bf16(tmem + TM::cP, dQ + off, dK + off, idQK, k > 0);
+            for (int i = 0; i < 8; ++i)
+              if (i < nk) {
+                const uint64_t off = st + (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4);
+                mma_bf16(tmem + TM::cP, dQ0 + off, dK0 + off, idQK, i > 0);
               }
             mma_commit(&bar[kQK]);
           }
           __syncwarp();
           return true;
         };
-        if (n_chunks > 0 && issue_qk(0)) {
-          for (int c = 0; c < n_chunks; ++c) {
-            const int st = c % L::kStages;
-            if (!wait(kSFull, c)) break;
-            if (c > 0 && !wait(kOFree, c - 1)) break;
+        if (next_chunk() && issue_qk(0)) {
+          for (int gc = 0; ok; ++gc) {
+            const uint64_t st = (uint64_t)((gc & 1) * kTile) >> 4;
+            const bool part = left == 0 && item_at(k)->n_last < C;
+            if (!wait(kSFull, gc)) break;
+            if (gc > 0 && !wait(kOFree, gc - 1)) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::Q + st * kTile), 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (k < nk) {
-                  const uint64_t off = (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4);
-                  mma_bf16(tmem + TM::cO, dQ + off, dS + off, idQS, k > 0);
+              for (int i = 0; i < 8; ++i)
+                if (i < nk) {
+                  const uint64_t off = (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4);
+                  mma_bf16(tmem + TM::cO, dQ0 + st + off, dS + off, idQS, i > 0);
                 }
               mma_commit(&bar[kSFree]);
             }
             __syncwarp();
-            if (!wait(kP, c)) break;
-            if (c + 1 == n_chunks && n_last < C && !wait(kFix, 0)) break;
+            if (!wait(kP, gc)) break;
+            if (part) {
+              if (!wait(kFix + (fixes & 1), fixes >> 1)) break;
+              ++fixes;
+            }
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t dV = sdesc_sw128(smem_u32(sm + L::V + st * kTile), kAtom, 1024);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_bf16_ts(tmem + TM::cO, tmem + TM::cP + 8 * k, dV + (uint64_t)((k * 2048) >> 4), idPV, 1);
+              for (int i = 0; i < 8; ++i)
+                mma_bf16_ts(tmem + TM::cO, tmem + TM::cP + 8 * i, dV0 + st + (uint64_t)((i * 2048) >> 4), idPV, 1);
               mma_commit(&bar[kOFull]);
-              mma_commit(&bar[kEmpty + st]);
+              mma_commit(&bar[kEmpty + (gc & 1)]);
             }
             __syncwarp();
-            if (c + 1 < n_chunks && !issue_qk(c + 1)) break;
+            ok = next_chunk() && issue_qk(gc + 1);
           }
         }
         if (elect_one()) mma_commit(&bar[kDrainA]);
@@ -722,36 +858,43 @@ __global__ void __launch_bounds__(NT, 1)
       // ---------------------------------------------------------- KV
       const uint32_t idKV = idesc_bf16(128, dkp, false, true);
       bool ok = true;
-      for (int c = 0; c < n_chunks && ok; ++c) {
-        const int st = c % L::kStages, kv = c % TM::kKVBufs;
-        const uint32_t d = tmem + TM::cKV + 128 * kv;
-        if (!(ok = wait(kFull + st, c / L::kStages))) break;
-        if (c + 1 == n_chunks && n_last < C && !(ok = wait(kFix, 0))) break;
-        if (c >= TM::kKVBufs && !(ok = wait(kKVFree + kv, c / TM::kKVBufs - 1))) break;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const int buf = q % TM::kABufs, m = c * (4 / TM::kABufs) + q / TM::kABufs;
-          if (!(ok = wait(kAFull + buf, m))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t dK = sdesc_sw128(smem_u32(sm + L::K + st * kTile), kAtom, 1024);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint64_t b = dK + (uint64_t)(((32 * q + 16 * k) * 128) >> 4);
-              const uint32_t a = tmem + TM::cA + buf * TM::ASTEP + 8 * k;
-              mma_bf16_ts(d, a + 48, b, idKV, q > 0 || k > 0);
-              mma_bf16_ts(d, a + 32, b, idKV, 1);
-              mma_bf16_ts(d, a + 16, b, idKV, 1);
-              mma_bf16_ts(d, a, b, idKV, 1);
-            }
-            mma_commit(&bar[kAFree + buf]);
-            if (q == 3) {
-              mma_commit(&bar[kKV + kv]);
-              mma_commit(&bar[kEmpty + st]);
-            }
+      for (int k = 0, gc = 0, fixes = 0; ok && get_item(k); ++k) {
+        const int n_chunks = item_at(k)->n_chunks;
+        for (int c = 0; c < n_chunks && ok; ++c, ++gc) {
+          const int st = gc % kStages, kv = gc % TM::kKVBufs;
+          const uint32_t d = tmem + TM::cKV + 128 * kv;
+          if (!(ok = wait(kFull + st, gc / kStages))) break;
+          if (c + 1 == n_chunks && item_at(k)->n_last < C) {
+            if (!(ok = wait(kFix + (fixes & 1), fixes >> 1))) break;
+            ++fixes;
           }
-          __syncwarp();
+          if (gc >= TM::kKVBufs && !(ok = wait(kKVFree + kv, gc / TM::kKVBufs - 1))) break;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const int buf = q % TM::kABufs, m = gc * (4 / TM::kABufs) + q / TM::kABufs;
+            if (!(ok = wait(kAFull + buf, m))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t dK = sdesc_sw128(smem_u32(sm + L::K + st * kTile), kAtom, 1024);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint64_t b = dK + (uint64_t)(((32 * q + 16 * i) * 128) >> 4);
+                const uint32_t a = tmem + TM::cA + buf * TM::ASTEP + 8 * i;
+                mma_bf16_ts(d, a + 48, b, idKV, q > 0 || i > 0);
+                mma_bf16_ts(d, a + 32, b, idKV, 1);
+                mma_bf16_ts(d, a + 16, b, idKV, 1);
+                mma_bf16_ts(d, a, b, idKV, 1);
+              }
+              mma_commit(&bar[kAFree + buf]);
+              if (q == 3) {
+                mma_commit(&bar[kKV + kv]);
+                mma_commit(&bar[kEmpty + st]);
+              }
+            }
+            __syncwarp();
+          }
         }
+        release_item(k);
       }
       if (elect_one()) mma_commit(&bar[kDrainB]);
       __syncwarp();
@@ -767,11 +910,14 @@ __global__ void __launch_bounds__(NT, 1)
         }
       }
       const uint32_t bytes = (uint32_t)((OUT ? 2 : 1) * dkp + dvp) * 256u;
-      auto store = [&](int c) {  // chunk c's outputs out of its stage of Q, which is then free
-        if (!wait(kStaged, c)) return false;
-        if (lane == 0) {
+      // Outputs staged in the two stages of V: first token and head, or h = -1 (part of a chunk, stored
+      // by the warps that staged it).
+      int t_old = 0, h_old = -1, t_new = 0, h_new = -1;
+      auto store = [&](int gc) {  // chunk gc's outputs, the older of the two, out of their stage, which is then free
+        if (!wait(kStaged + (gc & 1), gc >> 1)) return false;
+        if (lane == 0 && h_old >= 0) {
           for (int x = 0; x < dvp; x += 64)
-            tma_store_3d(&map_o, sm + L::Q + (c & 1) * kTile + (x >> 6) * kAtom, x, h, t_begin + c * C);
+            tma_store_3d(&map_o, sm + L::V + (gc & 1) * kTile + (x >> 6) * kAtom, x, h_old, t_old);
           bulk_commit();
           bulk_wait_read_all();
         }
@@ -779,34 +925,107 @@ __global__ void __launch_bounds__(NT, 1)
         return true;
       };
       bool ok = true;
-      for (int c = 0; c < n_chunks; ++c) {
-        const int st = c % L::kStages, t0 = t_begin + c * C;
-        if (c >= L::kStages && !(ok = wait(kEmpty + st, c / L::kStages - 1))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bar[kFull + st], bytes);
-          for (int x = 0; x < dkp; x += 64)
-            tma_load_3d(sm + L::K + st * kTile + (x >> 6) * kAtom, &map_k, &bar[kFull + st], x, hk, t0);
-          for (int x = 0; x < dvp; x += 64)
-            tma_load_3d(sm + L::V + st * kTile + (x >> 6) * kAtom, &map_v, &bar[kFull + st], x, h, t0);
-        }
-        __syncwarp();
-        if (OUT) {
-          const bool stored = c < 2 || (ok = store(c - 2));
-          if (lane == 0) {  // (loaded all the same, so that the stage's bytes are whole when a wait gave up)
-            for (int x = 0; x < dkp; x += 64)
-              tma_load_3d(sm + L::Q + st * kTile + (x >> 6) * kAtom, &map_q, &bar[kFull + st], x, hk, t0);
+      int gc = 0;
+      for (int k = 0; ok && get_item(k); ++k) {
+        const int n_chunks = item_at(k)->n_chunks, h = item_at(k)->h, hk = h / (p.h_v / p.h_k);
+        int t0 = item_at(k)->t_begin;
+        const bool part = item_at(k)->n_last < C;
+        for (int c = 0; c < n_chunks; ++c, ++gc, t0 += C) {
+          const int st = gc % kStages;
+          if (gc >= kStages && !(ok = wait(kEmpty + st, gc / kStages - 1))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar[kFull + st], bytes);
+            for (int x = 0; x < dkp; x += 64) {
+              if (OUT) tma_load_3d(sm + L::Q + st * kTile + (x >> 6) * kAtom, &map_q, &bar[kFull + st], x, hk, t0);
+              tma_load_3d(sm + L::K + st * kTile + (x >> 6) * kAtom, &map_k, &bar[kFull + st], x, hk, t0);
+            }
           }
-          if (!stored) {
-            if (lane == 0) *issued = c + 1;
+          __syncwarp();
+          if (OUT) {
+            if (gc >= 2) ok = store(gc - 2);
+            t_old = t_new;
+            h_old = h_new;
+            t_new = t0;
+            h_new = c + 1 == n_chunks && part ? -1 : h;
+          }
+          if (lane == 0) {  // (loaded all the same, so that the stage's bytes are whole when a wait gave up)
+            for (int x = 0; x < dvp; x += 64)
+              tma_load_3d(sm + L::V + st * kTile + (x >> 6) * kAtom, &map_v, &bar[kFull + st], x, h, t0);
+          }
+          if (lane == 0) *issued = gc + 1;
+          __syncwarp();
+          if (!ok) break;
+        }
+        release_item(k);
+      }
+      if (OUT && !*dead) {
+        if (gc >= 2 && store(gc - 2)) {
+          t_old = t_new;
+          h_old = h_new;
+          store(gc - 1);
+        } else if (gc == 1) {
+          t_old = t_new;
+          h_old = h_new;
+          store(0);
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- the work
+      int block = blockIdx.x, k = 0;
+      bool ok = true;
+      if (p.list) grid_dep_wait();  // the plan
+      for (int steals = 0; ok; ++steals) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar[kSteal], 16);
+          steal_block(sm + L::STEAL, &bar[kSteal]);
+        }
+        const int h = block % p.h_v, u = block / p.h_v;
+        const Segment s = p.list ? p.list[u] : only_segment(p, u);
+        if (!p.list && block == 0 && lane == 0 && s.seq < 0) atomicExch(p.status, GDN_ERR_SHAPE);
+        if (s.seq >= 0 && !(p.local_only && s.seg + 1 == s.n_seg)) {
+          if (k >= 2 && !(ok = wait(kItemFree + (k & 1), (k >> 1) - 1, kItemNs))) {
+            mbar_wait(&bar[kSteal], (uint32_t)(steals & 1), kWaitNs);  // (its answer is written here)
             break;
           }
+          const float g = p.log_decay[h];
+          float* cf = reinterpret_cast<float*>(sm + L::CF + 128 * (k & 1));
+          cf[lane] = lane == 31 ? 1.f : expf((float)(31 - lane) * g);
+          // Weight terms of a whole chunk: word 12 (4 q + j) + 4 term + e holds those of tokens
+          // 32 q + 8 e + 2 j + {0, 1}.
+          uint32_t* wtab = reinterpret_cast<uint32_t*>(sm + L::W + 768 * (k & 1));
+#pragma unroll 1
+          for (int i = lane; i < 64; i += 32) {
+            const int q = i >> 4, j = (i >> 2) & 3, e = i & 3;
+            uint32_t* w = wtab + 12 * (4 * q + j) + e;
+            weight_terms(C - 1 - (32 * q + 8 * e + 2 * j), g, w[0], w[4], w[8]);
+          }
+          if (lane == 0) {
+            Item* it = reinterpret_cast<Item*>(sm + L::ITEM + 64 * (k & 1));
+            const size_t whole = ((size_t)s.seq * p.h_v + h) * dd, part = ((size_t)s.local * p.h_v + h) * dd;
+            const bool cut = s.n_seg > 1;
+            it->n_chunks = (s.len + C - 1) / C;
+            it->t_begin = s.t_begin;
+            it->n_last = s.len > 0 ? (s.len - 1) % C + 1 : C;
+            it->h = h;
+            it->g = g;
+            it->S_in = cut ? (OUT ? p.local + part : nullptr) : p.S0 ? p.S0 + whole : nullptr;
+            const bool final = !cut || (OUT && s.seg + 1 == s.n_seg);
+            it->to_local = !final;
+            it->dst = final ? s.seq * p.h_v + h : OUT ? -1 : s.local * p.h_v + h;
+            if (it->S_in) bulk_prefetch_l2(it->S_in, (uint32_t)(dd * 4));
+          }
+          arrive(kItem + (k & 1));
+          ++k;
         }
-        if (lane == 0) *issued = c + 1;
+        if (!(ok = wait(kSteal, steals))) break;
+        if (!stolen_block(sm + L::STEAL, block)) break;
+        fence_async_smem();  // (the answer's bytes are read before the next one is asked for)
         __syncwarp();
       }
-      if (OUT && ok)
-        for (int c = max(0, n_chunks - 2); c < n_chunks; ++c)
-          if ((c + 1 < n_chunks || n_last == C) && !store(c)) break;
+      if (ok && (k < 2 || wait(kItemFree + (k & 1), (k >> 1) - 1, kItemNs))) {
+        if (lane == 0) reinterpret_cast<Item*>(sm + L::ITEM + 64 * (k & 1))->n_chunks = -1;
+        arrive(kItem + (k & 1));
+      }
     }
   }
   tc_fence_before();
@@ -815,8 +1034,8 @@ __global__ void __launch_bounds__(NT, 1)
     // A wait gave up: let the loads in flight land (each wait bounded; the MMAs were drained by their
     // issuing warps), then report.  The results are unspecified.
     if (tid == 0) {
-      for (int c = max(0, *issued - L::kStages); c < *issued; ++c)
-        mbar_wait(&bar[kFull + c % L::kStages], (uint32_t)((c / L::kStages) & 1), kWaitNs);
+      for (int c = max(0, *issued - kStages); c < *issued; ++c)
+        mbar_wait(&bar[kFull + c % kStages], (uint32_t)((c / kStages) & 1), kWaitNs);
       atomicExch(p.status, GDN_ERR_TIMEOUT);
     }
     __syncthreads();
@@ -830,25 +1049,32 @@ __global__ void __launch_bounds__(NT, 1)
 constexpr int kCarryNT = 256;
 template <bool FINAL>
 __global__ void __launch_bounds__(kCarryNT) linear_carry_kernel(const TcParams p) {
-  __shared__ int scratch[8];
-  const int h = blockIdx.x % p.h_v, seq = blockIdx.x / p.h_v;
-  const Unit un = find_unit(p.cu, p.n_seqs, p.total_tokens, p.seg_tokens, -1, seq, false, scratch);
-  if (un.seq < 0 || un.n_seg == 1) return;
+  const int h = blockIdx.x % p.h_v, i = blockIdx.x / p.h_v;
+  CutSeq q = {};
+  if (p.cuts) {
+    q = p.cuts[i];
+  } else {
+    const Segment s = only_segment(p, 0);
+    q.seq = s.seq;
+    q.n_seg = s.n_seg;
+    q.last_len = s.seq < 0 ? 0 : p.cu[1] - (p.cu[0] + (s.n_seg - 1) * p.seg_tokens);
+  }
+  if (q.seq < 0 || q.n_seg < 2) return;
   const float g = p.log_decay[h];
   const int dd = p.d_v * p.d_k;
   const int e = (blockIdx.y * kCarryNT + threadIdx.x) * 4;
   if (e >= dd) return;
-  const size_t at = ((size_t)seq * p.h_v + h) * dd + e;
+  const size_t at = ((size_t)q.seq * p.h_v + h) * dd + e;
   float4 E = p.S0 ? *reinterpret_cast<const float4*>(p.S0 + at) : make_float4(0.f, 0.f, 0.f, 0.f);
   const DecayStep step = decay_step(g, p.seg_tokens);
   const size_t stride = (size_t)p.h_v * dd;
-  float* loc = p.local + ((size_t)un.first * p.h_v + h) * dd + e;
-  for (int j = 0; j < un.n_seg; ++j, loc += stride) {
-    const bool last = j + 1 == un.n_seg;
+  float* loc = p.local + ((size_t)q.local * p.h_v + h) * dd + e;
+  for (int j = 0; j < q.n_seg; ++j, loc += stride) {
+    const bool last = j + 1 == q.n_seg;
     if (FINAL || !last) {
       const float4 x = *reinterpret_cast<const float4*>(loc);
       if (!FINAL) *reinterpret_cast<float4*>(loc) = E;
-      const DecayStep f = last ? decay_step(g, un.seq_end - (un.t_begin + j * p.seg_tokens)) : step;
+      const DecayStep f = last ? decay_step(g, q.last_len) : step;
       E = make_float4(f(E.x, x.x), f(E.y, x.y), f(E.z, x.z), f(E.w, x.w));
     } else {
       *reinterpret_cast<float4*>(loc) = E;
@@ -871,6 +1097,19 @@ bool make_map_heads(CUtensorMap* m, const void* base, int tokens, int heads, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// fp32 states [count][d_v][d_k], boxes of 32 x 32.
+bool make_map_states(CUtensorMap* m, const void* base, size_t count, int d_v, int d_k) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d_k, (cuuint64_t)d_v, (cuuint64_t)count};
+  cuuint64_t strides[2] = {(cuuint64_t)d_k * 4, (cuuint64_t)d_v * d_k * 4};
+  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -888,62 +1127,116 @@ int segment_tokens(int total_tokens, int h_v) {
   return seg >= total_tokens ? INT_MAX : std::max(seg, kMinSegment);
 }
 
+// What a call keeps in its workspace: the plan's lists (none for one sequence), the cut segments' states.
+struct Workspace {
+  int seg, units, cut_units, cuts;
+  size_t list, cut_list, cut_seqs, local, bytes;
+};
+Workspace workspace_of(const LinearParams& p) {
+  Workspace w = {};
+  const int seg = segment_tokens(p.total_tokens, p.h_v);
+  const bool cut = seg < p.total_tokens;
+  w.seg = cut ? seg : INT_MAX;
+  // sum of max(1, ceil(len / seg)) <= n + total / seg; a cut sequence is longer than seg
+  w.cuts = cut ? std::min(p.n_seqs, p.total_tokens / seg) : 0;
+  w.cut_units = cut ? w.cuts + p.total_tokens / seg : 0;
+  w.units = p.n_seqs + (cut ? p.total_tokens / seg : 0);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  if (p.n_seqs > 1) {
+    w.list = take(sizeof(Segment) * (size_t)w.units);
+    w.cut_list = take(sizeof(Segment) * (size_t)w.cut_units);
+    w.cut_seqs = take(sizeof(CutSeq) * (size_t)w.cuts);
+  }
+  w.local = take((size_t)w.cut_units * p.h_v * p.d_v * p.d_k * 4);
+  w.bytes = at;
+  return w;
+}
+
+template <bool OUT>
+cudaError_t launch_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                         const CUtensorMap& ms, const CUtensorMap& ml, const TcParams& p, int units, bool behind_plan, cudaStream_t stream) {
+  const void* kern = reinterpret_cast<const void*>(linear_tc_kernel<OUT>);
+  // (the warpgroups' shares add up to what the kernel is launched with: a smaller launch would wait)
+  cudaFuncAttributes have;
+  cudaError_t e = cudaFuncGetAttributes(&have, kern);
+  if (e != cudaSuccess) return e;
+  if (have.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<OUT>::TOTAL);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)units * p.h_v;
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = Lay<OUT>::TOTAL;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = behind_plan ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<OUT>, mq, mk, mv, mo, ms, ml, p);
+}
+
 }  // namespace
 
 bool linear_tc_supported(const LinearParams& p) { return p.total_tokens > 0; }
 
-size_t linear_tc_workspace_bytes(const LinearParams& p) {
-  const int seg = segment_tokens(p.total_tokens, p.h_v);
-  if (seg >= p.total_tokens) return 0;
-  return ((size_t)p.n_seqs + p.total_tokens / seg) * p.h_v * p.d_v * p.d_k * 4;
-}
+size_t linear_tc_workspace_bytes(const LinearParams& p) { return workspace_of(p).bytes; }
 
 cudaError_t launch_linear_tc(const LinearParams& lp, void* workspace, cudaStream_t stream) {
-  CUtensorMap mq{}, mk, mv, mo{};
+  CUtensorMap mq{}, mk, mv, mo{}, ms, ml{};
   if ((lp.write_O && (!make_map_heads(&mq, lp.q, lp.total_tokens, lp.h_k, lp.d_k) ||
                       !make_map_heads(&mo, lp.O, lp.total_tokens, lp.h_v, lp.d_v))) ||
       !make_map_heads(&mk, lp.k, lp.total_tokens, lp.h_k, lp.d_k) ||
       !make_map_heads(&mv, lp.v, lp.total_tokens, lp.h_v, lp.d_v))
     return cudaErrorInvalidValue;
+  const Workspace w = workspace_of(lp);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  if (!make_map_states(&ms, lp.S_out, (size_t)lp.n_seqs * lp.h_v, lp.d_v, lp.d_k) ||
+      (w.cut_units > 0 && !make_map_states(&ml, ws + w.local, (size_t)w.cut_units * lp.h_v, lp.d_v, lp.d_k)))
+    return cudaErrorInvalidValue;
   TcParams p{};
-  p.log_decay = lp.log_decay; p.cu = lp.cu; p.S0 = lp.S0; p.local = static_cast<float*>(workspace);
+  p.log_decay = lp.log_decay; p.cu = lp.cu; p.S0 = lp.S0; p.local = reinterpret_cast<float*>(ws + w.local);
   p.O = static_cast<__nv_bfloat16*>(lp.O); p.S_out = lp.S_out; p.status = lp.status;
   p.n_seqs = lp.n_seqs; p.total_tokens = lp.total_tokens; p.h_k = lp.h_k; p.h_v = lp.h_v; p.d_k = lp.d_k; p.d_v = lp.d_v;
   p.scale = lp.scale;
-  const int seg = segment_tokens(lp.total_tokens, lp.h_v);
-  const bool cut = seg < lp.total_tokens;
-  p.seg_tokens = cut ? seg : INT_MAX;
-  p.skip_last = cut && lp.write_O;
-  const long long units = (long long)lp.n_seqs + (cut ? lp.total_tokens / seg : 0);
-  const long long blocks = units * lp.h_v;
-  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<true>::ALLOC);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(linear_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<false>::ALLOC);
-  if (e != cudaSuccess) return e;
-  // (the warpgroups' shares add up to what the kernel is launched with: a smaller launch would wait)
-  cudaFuncAttributes attr;
-  for (const void* k : {reinterpret_cast<const void*>(linear_tc_kernel<true>), reinterpret_cast<const void*>(linear_tc_kernel<false>)}) {
-    e = cudaFuncGetAttributes(&attr, k);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-  }
-  if (cut || !lp.write_O) {
-    linear_tc_kernel<false><<<(unsigned)blocks, NT, Lay<false>::ALLOC, stream>>>(mq, mk, mv, mo, p);
+  p.seg_tokens = w.seg;
+  const bool cut = w.cuts > 0, plan = lp.n_seqs > 1;
+  Segment* list = plan ? reinterpret_cast<Segment*>(ws + w.list) : nullptr;
+  Segment* cut_list = plan ? reinterpret_cast<Segment*>(ws + w.cut_list) : nullptr;
+  CutSeq* cuts = plan ? reinterpret_cast<CutSeq*>(ws + w.cut_seqs) : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (plan) {
+    linear_plan_kernel<<<1, kPlanNT, 0, stream>>>(lp.cu, lp.n_seqs, lp.total_tokens, w.seg, list, w.units, cut_list,
+                                                  w.cut_units, cuts, w.cuts, lp.status);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
+  p.list = list;
+  p.cuts = cuts;
+  if (!lp.write_O) {
+    e = launch_items<false>(mq, mk, mv, mo, ms, ml, p, w.units, plan, stream);
+  } else if (cut) {
+    TcParams own = p;
+    own.list = cut_list;
+    own.local_only = 1;
+    e = launch_items<false>(mq, mk, mv, mo, ms, ml, own, w.cut_units, plan, stream);
+  }
+  if (e != cudaSuccess) return e;
   if (cut) {
-    const dim3 grid((unsigned)((long long)lp.n_seqs * lp.h_v), (lp.d_v * lp.d_k / 4 + kCarryNT - 1) / kCarryNT);
+    const dim3 grid((unsigned)(w.cuts * lp.h_v), (lp.d_v * lp.d_k / 4 + kCarryNT - 1) / kCarryNT);
     if (lp.write_O) linear_carry_kernel<false><<<grid, kCarryNT, 0, stream>>>(p);
     else linear_carry_kernel<true><<<grid, kCarryNT, 0, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (lp.write_O) {
-    linear_tc_kernel<true><<<(unsigned)blocks, NT, Lay<true>::ALLOC, stream>>>(mq, mk, mv, mo, p);
-    e = cudaGetLastError();
-  }
+  if (lp.write_O) e = launch_items<true>(mq, mk, mv, mo, ms, ml, p, w.units, plan && !cut, stream);
   return e;
 }
 
