@@ -176,20 +176,47 @@ def gdn_compose(T_list, Slocal_list, S_in=None, *, S_out=None, stream=None):
     return S_out
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {ref.device}")
+# The serving calls below run once per layer and token, so their checks and launches are kept to a few
+# microseconds: one comparison per tensor (the message is made only when it fails), no context manager
+# on the current device and stream, pointers as plain integers.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(device, stream):
-    """Context of a call on ``device`` and ``stream`` (None: its current stream): what the call
-    allocates then belongs to the stream that the kernels run on."""
-    if stream is None:
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
-    return torch.cuda.stream(stream)
+def _want(name, t, device, dtype, shape):
+    """data_ptr of t, a contiguous tensor of this shape and dtype on CUDA device ``device`` (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _need_cuda(name, t, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{device}")
+    return t.data_ptr()
+
+
+def _cuda_index(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _launch(call, where, device, stream, outputs, *args):
+    """Allocate the missing outputs ({name: (shape, dtype)} for None entries) and make the C call on
+    ``device`` and ``stream`` (None: the current one).  What is allocated here belongs to the stream that
+    the kernels run on."""
+    if stream is not None:
+        if stream.device.index != device:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{device}")
+        if stream != torch.cuda.current_stream(device) or torch.cuda.current_device() != device:
+            with torch.cuda.stream(stream):
+                return _launch(call, where, device, None, outputs, *args)
+    elif torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _launch(call, where, device, None, outputs, *args)
+    made = [t if not isinstance(t, tuple) else torch.empty(t[0], dtype=t[1], device=f"cuda:{device}") for t in outputs]
+    rc = call(*args, *[None if t is None else t.data_ptr() for t in made], _raw_stream(device))
+    if rc != _lib.GDN_OK:
+        _lib.check(rc, where)
+    return made
 
 
 def gdn_linear_attn(q, k, v, log_decay, cu_seqlens, S0=None, *, O_out=None, S_out=None, scale=1.0,
@@ -209,28 +236,18 @@ def gdn_linear_attn(q, k, v, log_decay, cu_seqlens, S0=None, *, O_out=None, S_ou
         raise ValueError(f"unsupported dtype {dt}")
     if q is None and not state_only:
         raise ValueError("q may be None only with state_only")
-    _need_cuda("q", q, dt, (T, h_k, d_k))
-    _need_cuda("k", k, dt)
-    _need_cuda("v", v, dt, (T, h_v, d_v))
-    _need_cuda("log_decay", log_decay, torch.float32, (h_v,))
-    _need_cuda("cu_seqlens", cu_seqlens, torch.int32, (n + 1,))
-    _need_cuda("S0", S0, torch.float32, (n, h_v, d_v, d_k))
-    _need_cuda("S_out", S_out, torch.float32, (n, h_v, d_v, d_k))
-    _need_cuda("O_out", O_out, dt, (T, h_v, d_v))
-    _same_device(k, q=q, v=v, log_decay=log_decay, cu_seqlens=cu_seqlens, S0=S0, S_out=S_out, O_out=O_out)
-    with _on(k.device, stream):
-        if S_out is None:
-            S_out = torch.empty((n, h_v, d_v, d_k), dtype=torch.float32, device=k.device)
-        if state_only:
-            O_out = None
-        elif O_out is None:
-            O_out = torch.empty((T, h_v, d_v), dtype=dt, device=k.device)
-        dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], _lib.GDN_STATE_ONLY if state_only else 0,
-                            float(scale))
-        rc = lib.gdn_linear_attn(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens),
-                                 _ptr(S0), _ptr(O_out), _ptr(S_out), _stream_handle(stream, k.device))
-    _lib.check(rc, "gdn_linear_attn")
-    return O_out, S_out
+    dev = _cuda_index("k", k)
+    qk, vo, state = (T, h_k, d_k), (T, h_v, d_v), (n, h_v, d_v, d_k)
+    args = (_want("q", q, dev, dt, qk), _want("k", k, dev, dt, qk), _want("v", v, dev, dt, vo),
+            _want("log_decay", log_decay, dev, torch.float32, (h_v,)),
+            _want("cu_seqlens", cu_seqlens, dev, torch.int32, (n + 1,)), _want("S0", S0, dev, torch.float32, state))
+    _want("O_out", O_out, dev, dt, vo)
+    _want("S_out", S_out, dev, torch.float32, state)
+    dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], _lib.GDN_STATE_ONLY if state_only else 0, scale)
+    O, S = _launch(lib.gdn_linear_attn, "gdn_linear_attn", dev, stream,
+                   (None if state_only else (vo, dt) if O_out is None else O_out,
+                    (state, torch.float32) if S_out is None else S_out), dims, *args)
+    return O, S
 
 
 def gdn_decode(q, k, v, g, beta, S_pool, slots=None, *, counts=None, O_out=None, l2norm_qk=True, scale=1.0,
@@ -256,37 +273,26 @@ def gdn_decode(q, k, v, g, beta, S_pool, slots=None, *, counts=None, O_out=None,
         raise ValueError("q may be None only with state_only")
     if n == 0 and T:
         raise ValueError(f"{T} tokens of no requests")
-    _need_cuda("q", q, dt, (T, h_k, d_k))
-    _need_cuda("k", k, dt)
-    _need_cuda("v", v, dt, (T, h_v, d_v))
-    _need_cuda("g", g, torch.float32, (h_v,) if head_decay else (T, h_v))
-    _need_cuda("beta", beta, torch.float32, (T, h_v))
-    _need_cuda("S_pool", S_pool, torch.float32, (n_slots, h_v, d_v, d_k))
-    _need_cuda("slots", slots, torch.int32, (n,))
-    _need_cuda("counts", counts, torch.int32, (n,))
-    _need_cuda("O_out", O_out, dt, (T, h_v, d_v))
-    _same_device(k, q=q, v=v, g=g, beta=beta, S_pool=S_pool, slots=slots, counts=counts, O_out=O_out)
+    dev = _cuda_index("k", k)
+    qk, vo, per = (T, h_k, d_k), (T, h_v, d_v), (T, h_v)
+    args = (n_slots, _want("q", q, dev, dt, qk), _want("k", k, dev, dt, qk), _want("v", v, dev, dt, vo),
+            _want("g", g, dev, torch.float32, (h_v,) if head_decay else per),
+            _want("beta", beta, dev, torch.float32, per), _want("slots", slots, dev, torch.int32, (n,)),
+            _want("counts", counts, dev, torch.int32, (n,)),
+            _want("S_pool", S_pool, dev, torch.float32, (n_slots, h_v, d_v, d_k)))
+    _want("O_out", O_out, dev, dt, vo)
     flags = (_lib.GDN_QK_L2NORM if l2norm_qk else 0) | (_lib.GDN_STATE_ONLY if state_only else 0) \
         | (_lib.GDN_SCALAR_DECAY if scalar_decay else 0) | (_lib.GDN_HEAD_DECAY if head_decay else 0) \
         | (_lib.GDN_KEEP_STATE if keep_state else 0)
-    with _on(k.device, stream):
-        if state_only:
-            O_out = None
-        elif O_out is None:
-            O_out = torch.empty((T, h_v, d_v), dtype=dt, device=k.device)
-        dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], flags, float(scale))
-        rc = lib.gdn_decode(ctypes.byref(dims), n_slots, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(slots),
-                            _ptr(counts), _ptr(S_pool), _ptr(O_out), _stream_handle(stream, k.device))
-    _lib.check(rc, "gdn_decode")
-    return O_out
+    dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], flags, scale)
+    return _launch(lib.gdn_decode, "gdn_decode", dev, stream,
+                   (None if state_only else (vo, dt) if O_out is None else O_out,), dims, *args)[0]
 
 
 def _prob_rows(name, t, shape):
     """Element stride between the rows of probabilities t [n, rows, vocab] (a vocabulary slice of
     padded rows will do; the rows must be evenly spaced)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
         return shape[2]
@@ -311,32 +317,26 @@ def gdn_verify_draft(target, drafted, uniforms, draft=None, draft_lens=None, *, 
     if target.dim() != 3:
         raise ValueError("target must be [n, n_draft + 1, vocab]")
     vocab = target.shape[2]
-    if target.dtype not in _DTYPE:
-        raise ValueError(f"unsupported dtype {target.dtype}")
+    dt = target.dtype
+    if dt not in _DTYPE:
+        raise ValueError(f"unsupported dtype {dt}")
+    dev = _cuda_index("target", target)
     target_stride = _prob_rows("target", target, (n, n_draft + 1, vocab))
-    draft_stride = 0
+    draft_stride, draft_ptr = 0, None
     if draft is not None:
-        if draft.dtype != target.dtype:
-            raise ValueError(f"draft must be {target.dtype}, got {draft.dtype}")
-        draft_stride = _prob_rows("draft", draft, (n, n_draft, vocab))
-    _need_cuda("drafted", drafted, torch.int32)
-    _need_cuda("uniforms", uniforms, torch.float32, (n, n_draft + 1))
-    _need_cuda("draft_lens", draft_lens, torch.int32, (n,))
-    _need_cuda("counts_out", counts_out, torch.int32, (n,))
-    _need_cuda("tokens_out", tokens_out, torch.int32, (n, n_draft + 1))
-    _same_device(target, draft=draft, drafted=drafted, uniforms=uniforms, draft_lens=draft_lens,
-                 counts_out=counts_out, tokens_out=tokens_out)
-    with _on(target.device, stream):
-        if counts_out is None:
-            counts_out = torch.empty((n,), dtype=torch.int32, device=target.device)
-        if tokens_out is None:
-            tokens_out = torch.empty((n, n_draft + 1), dtype=torch.int32, device=target.device)
-        dims = _lib.GdnVerifyDims(n, n_draft, vocab, _DTYPE[target.dtype], target_stride, draft_stride)
-        rc = lib.gdn_verify_draft(ctypes.byref(dims), _ptr(target), _ptr(draft), _ptr(drafted), _ptr(draft_lens),
-                                  _ptr(uniforms), _ptr(counts_out), _ptr(tokens_out),
-                                  _stream_handle(stream, target.device))
-    _lib.check(rc, "gdn_verify_draft")
-    return counts_out, tokens_out
+        if draft.dtype is not dt or draft.get_device() != dev:
+            raise ValueError(f"draft must be {dt} on cuda:{dev}, got {draft.dtype} on {draft.device}")
+        draft_stride, draft_ptr = _prob_rows("draft", draft, (n, n_draft, vocab)), draft.data_ptr()
+    i32, emitted = torch.int32, (n, n_draft + 1)
+    args = (target.data_ptr(), draft_ptr, _want("drafted", drafted, dev, i32, (n, n_draft)),
+            _want("draft_lens", draft_lens, dev, i32, (n,)), _want("uniforms", uniforms, dev, torch.float32, emitted))
+    _want("counts_out", counts_out, dev, i32, (n,))
+    _want("tokens_out", tokens_out, dev, i32, emitted)
+    dims = _lib.GdnVerifyDims(n, n_draft, vocab, _DTYPE[dt], target_stride, draft_stride)
+    counts, tokens = _launch(lib.gdn_verify_draft, "gdn_verify_draft", dev, stream,
+                             (((n,), i32) if counts_out is None else counts_out,
+                              (emitted, i32) if tokens_out is None else tokens_out), dims, *args)
+    return counts, tokens
 
 
 def gdn_get_status(stream=None, device=None):

@@ -5,26 +5,23 @@
 //   delta rule     S <- alpha S (I - beta k k^T) + beta v k^T
 //   scalar decay   S <- alpha S + beta v k^T
 //   head decay     S <- lambda_h S + v k^T
-// and the readout o = S (scale q) with the updated state.
-//
-// Every row s of S moves on its own: with a = s.k and b = s.q taken on the state before the token,
-//   d = beta (v_r - alpha a)   (no alpha a outside the delta rule),   s <- alpha s + d k,
-//   o_r = scale (alpha b + d k.q),
-// so one token needs one round of reductions (a and b together) instead of two.
+// and the readout o = S (scale q) with the updated state.  A window of up to W tokens is unrolled on
+// the state before it, so that a state is read, and written, once and every product with it stands
+// by itself: with a_t = S k_t, b_t = S q_t, R_it = alpha_{i+1} .. alpha_t and c_t = alpha_1 .. alpha_t
+//   d_t = beta_t (v_t - c_t a_t - sum_{i<t} R_it (k_i.k_t) d_i)        (delta rule; else beta_t v_t)
+//   o_t = c_t b_t + sum_{i<=t} R_it (k_i.q_t) d_i
+//   S  <- c_w S + sum_i R_iw d_i k_i^T
+// row by row of S: the products k_i.k_t, k_i.q_t are computed once per CTA, and a row's a_t, b_t are
+// reduced over the lanes that share it.  Longer windows go W tokens at a time, the state in registers.
 //
 // Layout: eight lanes share a row, lane l holding columns 4 (l & 7) + 32 j + [0, 4), so a warp's load
-// covers four rows in whole 128-byte lines and a reduction takes three shuffles.  A state is read once
-// into registers and written once, whatever the window's length.  Bound: HBM, 8 d_k d_v bytes per
-// (request, v-head) against about 6 d_k d_v flop a token.
+// covers four rows in whole 128-byte lines.  Bound: HBM, 8 d_k d_v bytes per (request, v-head).
 #include <cuda_bf16.h>
 
 #include "gdn_internal.cuh"
 
 namespace gdn {
 namespace {
-
-constexpr int NW = 8;         // warps per CTA
-constexpr int NT = 32 * NW;
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
@@ -39,17 +36,44 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
 }
-// Sum over the eight lanes of a row.
-__device__ __forceinline__ float sum8(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
-  x += __shfl_xor_sync(0xffffffffu, x, 4);
+// Two fp32 fused multiply-adds in one instruction (values as register pairs).
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float pair_sum(uint64_t x) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+  return a + b;
+}
+__device__ __forceinline__ float4 scale4(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// J: column groups of 32 (ceil(d_k / 32)); RG: groups of four rows per warp.
-template <typename Tin, int J, int RG>
-__global__ void __launch_bounds__(NT) decode_kernel(const DecodeParams p) {
+// A window's products of keys and queries are worth sharing over a whole state: sixteen warps for
+// windows, eight for single tokens.  Either way 32 warps per SM at 64 registers a thread: what these
+// kernels need most is loads in flight (256 requests of 32 heads, one token: 171 us, against 176 us at
+// 24 warps and 216 us at 16).
+__host__ __device__ constexpr int threads_of(int W) { return W == 1 ? 256 : 512; }
+
+// J: column groups of 32 (d_k at most 32 J); W: tokens unrolled at once; RG: groups of four rows per
+// warp (1 or 2).  DELTA: the delta rule.
+template <typename Tin, int J, int W, int RG, bool DELTA>
+__global__ void __launch_bounds__(threads_of(W), 1024 / threads_of(W)) decode_kernel(const DecodeParams p) {
+  constexpr int NT = threads_of(W), NW = NT / 32;
+  static_assert(W <= NW && (RG == 1 || RG == 2), "one warp prepares one token; two rows share eight lanes");
+  __shared__ __align__(16) float ks[W][kMaxHead], qs[W][kMaxHead];  // normalised, queries times scale
+  __shared__ float alpha[W], beta[W];
+  __shared__ __align__(16) float kk[W][W], kq[W][W];  // [t][i]: k_i.k_t and k_i.q_t times R_it
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i = blockIdx.x, h = blockIdx.y;
   const int slot = p.slots ? p.slots[i] : i;
@@ -70,7 +94,7 @@ __global__ void __launch_bounds__(NT) decode_kernel(const DecodeParams p) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int row = row0 + 4 * r, col = col0 + 32 * j;
-      s[r][j] = (row < p.d_v && col < p.d_k) ? *reinterpret_cast<const float4*>(Sb + (size_t)row * p.d_k + col)
+      s[r][j] = (row < p.d_v && col < p.d_k) ? __ldcs(reinterpret_cast<const float4*>(Sb + (size_t)row * p.d_k + col))
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   // Two requests on one slot would race on its state: the first of them has it, the others are
@@ -83,96 +107,187 @@ __global__ void __launch_bounds__(NT) decode_kernel(const DecodeParams p) {
       return;
     }
   }
-  const float head_alpha = p.family == kHeadDecay ? expf(p.g[h]) : 0.f;
+  const bool want_o = !p.state_only;
   const Tin* qp = static_cast<const Tin*>(p.q);
   const Tin* kp = static_cast<const Tin*>(p.k);
   const Tin* vp = static_cast<const Tin*>(p.v);
   Tin* op = static_cast<Tin*>(p.O);
-  for (int t = 0; t < cnt; ++t) {
-    const size_t tok = (size_t)i * p.window + t;
-    float4 k[J], q[J];
-    float kk = 0.f, qq = 0.f, kq = 0.f;
+  // the row whose sums this lane ends up with
+  const int my_r = RG == 2 ? (lane >> 2) & 1 : 0;
+  const int my_row = row0 + 4 * my_r;
+  // products of this lane group's rows with x (this lane's columns), summed over a row's eight lanes;
+  // with two rows, half of the lanes end up with each
+  auto row_sum = [&](const float* x) {
+    uint64_t y2[RG];
+#pragma unroll
+    for (int r = 0; r < RG; ++r) y2[r] = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int col = col0 + 32 * j;
-      const bool in = col < p.d_k;
-      k[j] = in ? load4(kp + (tok * p.h_k + hk) * p.d_k + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-      q[j] = in && !p.state_only ? load4(qp + (tok * p.h_k + hk) * p.d_k + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float v[RG];
+      const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(x + 32 * j);
 #pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      const int row = row0 + 4 * r;
-      v[r] = row < p.d_v ? load1(vp + (tok * p.h_v + h) * p.d_v + row) : 0.f;
+      for (int r = 0; r < RG; ++r)
+        y2[r] = fma2(pair(s[r][j].z, s[r][j].w), u.y, fma2(pair(s[r][j].x, s[r][j].y), u.x, y2[r]));
     }
-    const float alpha = p.family == kHeadDecay ? head_alpha : expf(p.g[tok * p.h_v + h]);
-    const float beta = p.family == kHeadDecay ? 1.f : p.beta[tok * p.h_v + h];
+    float y[RG];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      kk = dot4(k[j], k[j], kk);
-      qq = dot4(q[j], q[j], qq);
-      kq = dot4(k[j], q[j], kq);
+    for (int r = 0; r < RG; ++r) y[r] = pair_sum(y2[r]);
+    float z = my_r ? y[RG - 1] : y[0];
+    z += __shfl_xor_sync(0xffffffffu, RG == 2 && !my_r ? y[RG - 1] : y[0], 4);
+    z += __shfl_xor_sync(0xffffffffu, z, 2);
+    return z + __shfl_xor_sync(0xffffffffu, z, 1);
+  };
+  for (int t0 = 0; t0 < cnt; t0 += W) {
+    const int m = min(W, cnt - t0);
+    const size_t tok0 = (size_t)i * p.window + t0;
+    float v[W];
+#pragma unroll
+    for (int t = 0; t < W; ++t)
+      v[t] = t < m && my_row < p.d_v ? load1(vp + ((tok0 + t) * p.h_v + h) * p.d_v + my_row) : 0.f;
+    if (t0 > 0) __syncthreads();  // the tables of the tokens before are read
+    if (warp < m) {
+      const size_t tok = tok0 + warp;
+      const bool in = 4 * lane < p.d_k;
+      float4 k = make_float4(0.f, 0.f, 0.f, 0.f), q = k;
+      if (in) {
+        k = load4(kp + (tok * p.h_k + hk) * p.d_k + 4 * lane);
+        if (want_o) q = load4(qp + (tok * p.h_k + hk) * p.d_k + 4 * lane);
+      }
+      if (lane == 0) {
+        alpha[warp] = expf(p.family == kHeadDecay ? p.g[h] : p.g[tok * p.h_v + h]);
+        beta[warp] = p.family == kHeadDecay ? 1.f : p.beta[tok * p.h_v + h];
+      }
+      float rk = 1.f, rq = p.scale;
+      if (p.l2norm) {
+        rk = 1.f / sqrtf(warp_sum(dot4(k, k, 0.f)) + 1e-6f);
+        if (want_o) rq *= 1.f / sqrtf(warp_sum(dot4(q, q, 0.f)) + 1e-6f);
+      }
+      k = scale4(k, rk);
+      q = scale4(q, rq);
+      *reinterpret_cast<float4*>(&ks[warp][4 * lane]) = k;
+      *reinterpret_cast<float4*>(&qs[warp][4 * lane]) = q;
     }
-    kk = sum8(kk);
-    qq = sum8(qq);
-    kq = sum8(kq);
-    const float rk = p.l2norm ? 1.f / sqrtf(kk + 1e-6f) : 1.f;
-    const float rq = (p.l2norm ? 1.f / sqrtf(qq + 1e-6f) : 1.f) * p.scale;
-#pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      float a = 0.f, b = 0.f;
+    __syncthreads();
+    // Products of the window's keys with its keys and queries: eight lanes a pair.
+#pragma unroll 1
+    for (int e0 = 4 * warp; e0 < W * W; e0 += 4 * NW) {
+      const int e = min(e0 + (lane >> 3), W * W - 1), a = e % W, t = e / W;
+      uint64_t x2 = 0, y2 = 0;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        a = dot4(s[r][j], k[j], a);
-        b = dot4(s[r][j], q[j], b);
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&ks[a][col0 + 32 * j]);
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&ks[t][col0 + 32 * j]);
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&qs[t][col0 + 32 * j]);
+        x2 = fma2(u.y, k.y, fma2(u.x, k.x, x2));
+        y2 = fma2(u.y, q.y, fma2(u.x, q.x, y2));
       }
-      a = sum8(a) * rk;
-      b = sum8(b);
-      const float d = beta * (p.family == kDelta ? fmaf(-alpha, a, v[r]) : v[r]) * rk;  // along the raw key
+      float x = pair_sum(x2), y = pair_sum(y2);
+#pragma unroll
+      for (int o = 1; o <= 4; o <<= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+      }
+      if ((lane & 7) == 0 && a <= t && t < m) {
+        float R = 1.f;
+        for (int j = a + 1; j <= t; ++j) R *= alpha[j];
+        kk[t][a] = R * x;
+        kq[t][a] = R * y;
+      }
+    }
+    // a_t = S k_t and b_t = S q_t: this lane's columns for all its rows, then the sums over a row's
+    // eight lanes; with two rows, half of the lanes end up with each.
+    float am[W], bm[W], d[W];
+#pragma unroll
+    for (int t = 0; t < W; ++t) {
+      am[t] = bm[t] = 0.f;
+      if (t >= m) continue;
+      if (DELTA) am[t] = row_sum(&ks[t][col0]);
+      if (want_o) bm[t] = row_sum(&qs[t][col0]);
+    }
+    __syncthreads();  // kk, kq
+    float c = 1.f;
+#pragma unroll
+    for (int t = 0; t < W; ++t) {
+      d[t] = 0.f;
+      if (t >= m) continue;
+      c *= alpha[t];
+      float x = v[t];
+      if (DELTA) {
+        x = fmaf(-c, am[t], x);
+#pragma unroll
+        for (int e = 0; e < t; ++e) x = fmaf(-kk[t][e], d[e], x);
+      }
+      d[t] = beta[t] * x;
+      if (want_o) {
+        float o = c * bm[t];
+#pragma unroll
+        for (int e = 0; e <= t; ++e) o = fmaf(kq[t][e], d[e], o);
+        // (of the lanes that hold the row's sums, another one writes each token)
+        if ((lane & 3) == (t & 3) && (RG == 2 || (lane & 4) == 0) && my_row < p.d_v)
+          store1(op + ((tok0 + t) * p.h_v + h) * p.d_v + my_row, o);
+      }
+    }
+    if (p.keep && t0 + W >= cnt) return;
+    // S <- c S + sum_t R_t d_t k_t^T
+    float R = 1.f;
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int j = 0; j < J; ++j) s[r][j] = scale4(s[r][j], c);
+#pragma unroll
+    for (int t = W - 1; t >= 0; --t) {
+      if (t >= m) continue;
+      const float x = R * d[t], y = RG == 2 ? __shfl_xor_sync(0xffffffffu, x, 4) : 0.f;
+      R *= alpha[t];
+      const float x0 = my_r ? y : x, x1 = my_r ? x : y;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        s[r][j].x = fmaf(alpha, s[r][j].x, d * k[j].x);
-        s[r][j].y = fmaf(alpha, s[r][j].y, d * k[j].y);
-        s[r][j].z = fmaf(alpha, s[r][j].z, d * k[j].z);
-        s[r][j].w = fmaf(alpha, s[r][j].w, d * k[j].w);
+        const float4 k = *reinterpret_cast<const float4*>(&ks[t][col0 + 32 * j]);
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          const float f = r == 0 ? x0 : x1;
+          s[r][j] = make_float4(fmaf(f, k.x, s[r][j].x), fmaf(f, k.y, s[r][j].y), fmaf(f, k.z, s[r][j].z),
+                                fmaf(f, k.w, s[r][j].w));
+        }
       }
-      const int row = row0 + 4 * r;
-      if (!p.state_only && (lane & 7) == 0 && row < p.d_v)
-        store1(op + (tok * p.h_v + h) * p.d_v + row, rq * fmaf(alpha, b, d * kq));
     }
   }
-  if (p.keep) return;
 #pragma unroll
   for (int r = 0; r < RG; ++r)
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int row = row0 + 4 * r, col = col0 + 32 * j;
-      if (row < p.d_v && col < p.d_k) *reinterpret_cast<float4*>(Sb + (size_t)row * p.d_k + col) = s[r][j];
+      if (row < p.d_v && col < p.d_k) __stcs(reinterpret_cast<float4*>(Sb + (size_t)row * p.d_k + col), s[r][j]);
     }
 }
 
-template <typename Tin, int J, int RG>
+template <typename Tin, int J, int W, int RG, bool DELTA>
 cudaError_t launch(const DecodeParams& p, cudaStream_t stream) {
-  const int rows = NW * 4 * RG;
+  constexpr int NT = threads_of(W), rows = NT / 32 * 4 * RG;
   const dim3 grid(p.n, p.h_v, (p.d_v + rows - 1) / rows);
-  decode_kernel<Tin, J, RG><<<grid, NT, 0, stream>>>(p);
+  decode_kernel<Tin, J, W, RG, DELTA><<<grid, NT, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <typename Tin, int RG>
-cudaError_t launch_cols(const DecodeParams& p, cudaStream_t stream) {
-  switch ((p.d_k + 31) / 32) {
-    case 1: return launch<Tin, 1, RG>(p, stream);
-    case 2: return launch<Tin, 2, RG>(p, stream);
-    case 3: return launch<Tin, 3, RG>(p, stream);
-    default: return launch<Tin, 4, RG>(p, stream);
-  }
+template <typename Tin, int J, int W>
+cudaError_t launch_rows(const DecodeParams& p, cudaStream_t stream) {
+  const bool few = (long long)p.n * p.h_v < 152;
+  if (p.family == kDelta) return few ? launch<Tin, J, W, 1, true>(p, stream) : launch<Tin, J, W, 2, true>(p, stream);
+  return few ? launch<Tin, J, W, 1, false>(p, stream) : launch<Tin, J, W, 2, false>(p, stream);
+}
+
+template <typename Tin>
+cudaError_t launch_shape(const DecodeParams& p, cudaStream_t stream) {
+  if (p.d_k <= 64)
+    return p.window == 1 ? launch_rows<Tin, 2, 1>(p, stream)
+           : p.window <= 4 ? launch_rows<Tin, 2, 4>(p, stream) : launch_rows<Tin, 2, 8>(p, stream);
+  return p.window == 1 ? launch_rows<Tin, 4, 1>(p, stream)
+         : p.window <= 4 ? launch_rows<Tin, 4, 4>(p, stream) : launch_rows<Tin, 4, 8>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode(const DecodeParams& p, int bf16, cudaStream_t stream) {
-  return bf16 ? launch_cols<__nv_bfloat16, 4>(p, stream) : launch_cols<float, 4>(p, stream);
+  return bf16 ? launch_shape<__nv_bfloat16>(p, stream) : launch_shape<float>(p, stream);
 }
 
 }  // namespace gdn

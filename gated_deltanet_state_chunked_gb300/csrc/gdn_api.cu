@@ -1,6 +1,7 @@
 // C ABI of libgdn.so: argument checks, dispatch to the kernels, status word.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdio>
 #include <cstring>
 #include <cstdarg>
@@ -135,8 +136,14 @@ unsigned long long take_wait_limit_ns() {
 }
 
 int* device_status_word() {
-  void* p = nullptr;
+  static std::atomic<void*> known[64];  // per device (the symbol's address on it)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  const bool keep = dev >= 0 && dev < 64;
+  void* p = keep ? known[dev].load(std::memory_order_acquire) : nullptr;
+  if (p) return static_cast<int*>(p);
   if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
+  if (keep) known[dev].store(p, std::memory_order_release);
   return static_cast<int*>(p);
 }
 
@@ -301,9 +308,10 @@ int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const vo
   if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dims->dtype == GDN_BF16 && linear_tc_supported(p)) {
-    const size_t bytes = linear_tc_workspace_bytes(p);
+    size_t bytes = 0;
     void* ws = nullptr;
-    cudaError_t e = cudaSuccess, ef = cudaSuccess;
+    cudaError_t e = linear_tc_workspace_bytes(p, &bytes), ef = cudaSuccess;
+    if (e != cudaSuccess) return cuda_fail(e, "gdn_linear_attn set-up");
     if (bytes) {
       cudaMemPool_t pool = nullptr;
       rc = scratch_pool(&pool);

@@ -119,9 +119,9 @@ struct LinearParams {
   int write_O;
   float scale;
 };
-// Tensor-core path (bf16 inputs, total_tokens > 0); workspace: linear_tc_workspace_bytes(), may be 0.
+// Tensor-core path (bf16 inputs, total_tokens > 0); workspace: linear_tc_workspace_bytes, may be 0.
 bool linear_tc_supported(const LinearParams& p);
-size_t linear_tc_workspace_bytes(const LinearParams& p);
+cudaError_t linear_tc_workspace_bytes(const LinearParams& p, size_t* bytes);
 cudaError_t launch_linear_tc(const LinearParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_linear_simt(const LinearParams& p, int bf16, cudaStream_t stream);
 

@@ -47,6 +47,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "gdn_internal.cuh"
@@ -62,7 +63,7 @@ using tcp::kWaitNs;
 constexpr int C = 128;           // tokens per chunk
 constexpr int NWARP = 28, NT = 32 * NWARP;
 constexpr int kRegsLaunch = 72;  // a thread's registers at launch, and (below) in its warpgroup's role
-constexpr int kRegsRows = 72, kRegsSplit = 56, kRegsState = 104, kRegsControl = 40;
+constexpr int kRegsRows = 72, kRegsSplit = 56, kRegsState = 96, kRegsControl = 56;
 static_assert(2 * kRegsRows + 2 * kRegsSplit + 2 * kRegsState + kRegsControl <= 7 * kRegsLaunch &&
               4 * kRegsSplit + 2 * kRegsState + kRegsControl <= 7 * kRegsLaunch, "what a launch holds");
 constexpr uint32_t kTile = 32768, kAtom = 16384;  // 128 rows x 128 bf16: two swizzled atoms of 64 columns
@@ -1110,19 +1111,40 @@ bool make_map_states(CUtensorMap* m, const void* base, size_t count, int d_v, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 152;
-  return sms;
-}
-
 constexpr int kMinSegment = 512;
 
+// What the launches need to know of a device, looked up once: its SMs, and that the kernels may have
+// their shared memory and are launched with the registers that the warpgroups' shares add up to (with
+// fewer, a warpgroup that asks for more would wait).
+cudaError_t prepare_device(int* sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+  *sms = known[dev].load(std::memory_order_acquire);
+  if (*sms > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const void* kernels[] = {reinterpret_cast<const void*>(linear_tc_kernel<true>),
+                           reinterpret_cast<const void*>(linear_tc_kernel<false>)};
+  const int bytes[] = {(int)Lay<true>::TOTAL, (int)Lay<false>::TOTAL};
+  for (int i = 0; i < 2; ++i) {
+    cudaFuncAttributes have;
+    e = cudaFuncGetAttributes(&have, kernels[i]);
+    if (e != cudaSuccess) return e;
+    if (have.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+    e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]);
+    if (e != cudaSuccess) return e;
+  }
+  known[dev].store(*sms, std::memory_order_release);
+  return cudaSuccess;
+}
+
 // Tokens per segment: one sequence's segments times the v-heads fill the GPU once.
-int segment_tokens(int total_tokens, int h_v) {
-  const int parts = std::max(1, device_sms() / h_v);
+int segment_tokens(int total_tokens, int h_v, int sms) {
+  const int parts = std::max(1, sms / h_v);
   const int seg = ((total_tokens + parts - 1) / parts + C - 1) / C * C;
   return seg >= total_tokens ? INT_MAX : std::max(seg, kMinSegment);
 }
@@ -1132,9 +1154,9 @@ struct Workspace {
   int seg, units, cut_units, cuts;
   size_t list, cut_list, cut_seqs, local, bytes;
 };
-Workspace workspace_of(const LinearParams& p) {
+Workspace workspace_of(const LinearParams& p, int sms) {
   Workspace w = {};
-  const int seg = segment_tokens(p.total_tokens, p.h_v);
+  const int seg = segment_tokens(p.total_tokens, p.h_v, sms);
   const bool cut = seg < p.total_tokens;
   w.seg = cut ? seg : INT_MAX;
   // sum of max(1, ceil(len / seg)) <= n + total / seg; a cut sequence is longer than seg
@@ -1160,14 +1182,6 @@ Workspace workspace_of(const LinearParams& p) {
 template <bool OUT>
 cudaError_t launch_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                          const CUtensorMap& ms, const CUtensorMap& ml, const TcParams& p, int units, bool behind_plan, cudaStream_t stream) {
-  const void* kern = reinterpret_cast<const void*>(linear_tc_kernel<OUT>);
-  // (the warpgroups' shares add up to what the kernel is launched with: a smaller launch would wait)
-  cudaFuncAttributes have;
-  cudaError_t e = cudaFuncGetAttributes(&have, kern);
-  if (e != cudaSuccess) return e;
-  if (have.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<OUT>::TOTAL);
-  if (e != cudaSuccess) return e;
   const long long blocks = (long long)units * p.h_v;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -1187,16 +1201,24 @@ cudaError_t launch_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 
 bool linear_tc_supported(const LinearParams& p) { return p.total_tokens > 0; }
 
-size_t linear_tc_workspace_bytes(const LinearParams& p) { return workspace_of(p).bytes; }
+cudaError_t linear_tc_workspace_bytes(const LinearParams& p, size_t* bytes) {
+  int sms = 0;
+  const cudaError_t e = prepare_device(&sms);
+  if (e == cudaSuccess) *bytes = workspace_of(p, sms).bytes;
+  return e;
+}
 
 cudaError_t launch_linear_tc(const LinearParams& lp, void* workspace, cudaStream_t stream) {
+  int sms = 0;
+  cudaError_t e = prepare_device(&sms);
+  if (e != cudaSuccess) return e;
   CUtensorMap mq{}, mk, mv, mo{}, ms, ml{};
   if ((lp.write_O && (!make_map_heads(&mq, lp.q, lp.total_tokens, lp.h_k, lp.d_k) ||
                       !make_map_heads(&mo, lp.O, lp.total_tokens, lp.h_v, lp.d_v))) ||
       !make_map_heads(&mk, lp.k, lp.total_tokens, lp.h_k, lp.d_k) ||
       !make_map_heads(&mv, lp.v, lp.total_tokens, lp.h_v, lp.d_v))
     return cudaErrorInvalidValue;
-  const Workspace w = workspace_of(lp);
+  const Workspace w = workspace_of(lp, sms);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   if (!make_map_states(&ms, lp.S_out, (size_t)lp.n_seqs * lp.h_v, lp.d_v, lp.d_k) ||
       (w.cut_units > 0 && !make_map_states(&ml, ws + w.local, (size_t)w.cut_units * lp.h_v, lp.d_v, lp.d_k)))
@@ -1211,7 +1233,6 @@ cudaError_t launch_linear_tc(const LinearParams& lp, void* workspace, cudaStream
   Segment* list = plan ? reinterpret_cast<Segment*>(ws + w.list) : nullptr;
   Segment* cut_list = plan ? reinterpret_cast<Segment*>(ws + w.cut_list) : nullptr;
   CutSeq* cuts = plan ? reinterpret_cast<CutSeq*>(ws + w.cut_seqs) : nullptr;
-  cudaError_t e = cudaSuccess;
   if (plan) {
     linear_plan_kernel<<<1, kPlanNT, 0, stream>>>(lp.cu, lp.n_seqs, lp.total_tokens, w.seg, list, w.units, cut_list,
                                                   w.cut_units, cuts, w.cuts, lp.status);
