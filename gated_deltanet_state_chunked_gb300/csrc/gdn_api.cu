@@ -307,26 +307,21 @@ int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const vo
   p.status = device_status_word();
   if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dims->dtype == GDN_BF16 && linear_tc_supported(p)) {
-    size_t bytes = 0;
-    void* ws = nullptr;
-    cudaError_t e = linear_tc_workspace_bytes(p, &bytes), ef = cudaSuccess;
-    if (e != cudaSuccess) return cuda_fail(e, "gdn_linear_attn set-up");
-    if (bytes) {
-      cudaMemPool_t pool = nullptr;
-      rc = scratch_pool(&pool);
-      if (rc) return rc;
-      e = cudaMallocFromPoolAsync(&ws, bytes, pool, st);
-      if (e != cudaSuccess) return fail(GDN_ERR_NOMEM, "scratch of %zu bytes: %s", bytes, cudaGetErrorString(e));
-    }
-    e = launch_linear_tc(p, ws, st);
-    if (ws) ef = cudaFreeAsync(ws, st);
-    if (e != cudaSuccess) return cuda_fail(e, "gdn_linear_attn tensor-core launch");
-    if (ef != cudaSuccess) return cuda_fail(ef, "scratch release");
-    return GDN_OK;
+  size_t bytes = 0;
+  void* ws = nullptr;
+  cudaError_t e = linear_workspace_bytes(p, dims->dtype == GDN_BF16, &bytes), ef = cudaSuccess;
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_linear_attn set-up");
+  if (bytes) {
+    cudaMemPool_t pool = nullptr;
+    rc = scratch_pool(&pool);
+    if (rc) return rc;
+    e = cudaMallocFromPoolAsync(&ws, bytes, pool, st);
+    if (e != cudaSuccess) return fail(GDN_ERR_NOMEM, "scratch of %zu bytes: %s", bytes, cudaGetErrorString(e));
   }
-  const cudaError_t e = launch_linear_simt(p, dims->dtype == GDN_BF16, st);
+  e = launch_linear(p, dims->dtype == GDN_BF16, ws, st);
+  if (ws) ef = cudaFreeAsync(ws, st);
   if (e != cudaSuccess) return cuda_fail(e, "gdn_linear_attn launch");
+  if (ef != cudaSuccess) return cuda_fail(ef, "scratch release");
   return GDN_OK;
 }
 

@@ -119,11 +119,9 @@ struct LinearParams {
   int write_O;
   float scale;
 };
-// Tensor-core path (bf16 inputs, total_tokens > 0); workspace: linear_tc_workspace_bytes, may be 0.
-bool linear_tc_supported(const LinearParams& p);
-cudaError_t linear_tc_workspace_bytes(const LinearParams& p, size_t* bytes);
-cudaError_t launch_linear_tc(const LinearParams& p, void* workspace, cudaStream_t stream);
-cudaError_t launch_linear_simt(const LinearParams& p, int bf16, cudaStream_t stream);
+// Scratch that a call needs on the current device (may be 0), and the call.
+cudaError_t linear_workspace_bytes(const LinearParams& p, int bf16, size_t* bytes);
+cudaError_t launch_linear(const LinearParams& p, int bf16, void* workspace, cudaStream_t stream);
 
 // S <- lambda^n S + D of a carried state, lambda = exp(g).  A factor near 1 stored in fp32 is off by
 // up to 2^-25, always the same way, and a long prompt multiplies by it hundreds of times; the step

@@ -1,185 +1,259 @@
-// Linear attention with a decay for each head over packed prompts, on the CUDA cores in fp32: fp32
-// inputs of any head size.
+// Linear attention with a decay for each head over packed prompts, fp32 inputs, on the CUDA cores.
 //
 // Method: the scalar-decay family that "LinearKV: One Cached State Suffices for Position-Independent
 // Caching in Hybrid LLMs" (composition passage) sets beside the delta rule, with a decay lambda_h that
 // belongs to the head:  S_t = lambda_h S_{t-1} + v_t k_t^T,  o_t = S_t (scale q_t).  Chunk by chunk
 // (64 tokens, n of them in the last one) with the entering state S:
-//   P_ts = scale lambda^(t-s) q_t.k_s   (s <= t)
-//   O_t  = sum_s P_ts v_s + scale lambda^(t+1) S q_t
+//   P_ts = lambda^(t-s) q_t.k_s   (s <= t)
+//   O_t  = scale (sum_s P_ts v_s + lambda^(t+1) S q_t)
 //   S   <- lambda^n S + sum_s lambda^(n-1-s) v_s k_s^T
-// One CTA owns 32 rows of one (sequence, v-head) state and walks the sequence's chunks.
-#include <cuda_bf16.h>
-
-#include "gdn_internal.cuh"
+// One CTA owns a (segment, v-head) and walks its chunks.  The state stays in registers, up to 8 x 8 entries
+// a thread, and is copied to shared memory, transposed, as the
+// readout's operand.  Every product is a register tile fed from shared memory: 4 x 4 for P (blocks above
+// the diagonal skipped), 8 rows x 4 columns for O, 8 x 8 for S, so that a fused multiply-add costs at
+// most three quarters of a shared-memory wavefront and the fp32 pipes are the bound.
+#include "linear_work.cuh"
 #include "tc_common.cuh"
 
 namespace gdn {
 namespace {
 
-using tcp::chunk_info;
-using tcp::ChunkInfo;
-
-constexpr int C = kChunk, R = 32, NT = 256;
-constexpr int QS = kMaxHead + 4;  // row strides (floats) of the tiles
-constexpr int PS = C + 4, VS = R + 4;
+constexpr int C = kChunk, D = kMaxHead, NT = 256;
+constexpr int TS = D + 4;  // row stride (floats) of Q, K, V and of the state's copy
+constexpr int PS = C + 4;
 
 struct Smem {
-  float Q[C * QS], K[C * QS], S[R * QS], P[C * PS], V[C * VS], W[C * VS];
+  float Q[C * TS], K[C * TS], V[C * TS], St[D * TS], P[C * PS];
   float pw[C + 1];  // lambda^n
-  int scratch[32];
 };
-
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
 }
+// 16 bytes of global memory into shared memory, or zeros.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+  const int bytes = there ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-template <typename Tin>
-__global__ void __launch_bounds__(NT) linear_simt_kernel(const LinearParams p) {
+// JN: groups of 16 state columns (d_k at most 16 JN); RI: state rows a thread (d_v at most 16 RI), 8 or 4,
+// and as many rows of O (at 4 a warp's halves take four rows each).
+template <bool OUT, int JN, int RI>
+__global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) {
   extern __shared__ __align__(16) unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int seq = blockIdx.x, h = blockIdx.y, r0 = blockIdx.z * R;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = tid & 15, y = tid >> 4;
+  const int h = blockIdx.x % p.h_v, u = blockIdx.x / p.h_v;
+  if (p.list) tc::grid_dep_wait();  // the plan
+  const Segment seg = p.list ? p.list[u] : only_segment(p, u);
+  if (!p.list && blockIdx.x == 0 && tid == 0 && seg.seq < 0) atomicExch(p.status, GDN_ERR_SHAPE);
+  if (seg.seq < 0 || (p.local_only && seg.seg + 1 == seg.n_seg)) return;
+  const ItemState state = item_state(p, seg, h, OUT);
   const int d_k = p.d_k, d_v = p.d_v, hk = h / (p.h_v / p.h_k);
-  const ChunkInfo ci = chunk_info(p.cu, p.n_seqs, p.total_tokens, seq, -1, sm.scratch);
-  if (!ci.valid) {
-    if (tid == 0) atomicExch(p.status, GDN_ERR_SHAPE);
-    return;
-  }
-  const int t_begin = p.cu[seq], t_end = p.cu[seq + 1];
   const float g = p.log_decay[h];
-  for (int n = tid; n <= C; n += NT) sm.pw[n] = n ? expf((float)n * g) : 1.f;
-  float* S_out = p.S_out + ((size_t)seq * p.h_v + h) * d_v * d_k;
-  const float* S0 = p.S0 ? p.S0 + ((size_t)seq * p.h_v + h) * d_v * d_k : nullptr;
-  for (int e = tid; e < R * d_k; e += NT) {
-    const int r = e / d_k, c = e % d_k;
-    sm.S[r * QS + c] = S0 && r0 + r < d_v ? S0[(size_t)(r0 + r) * d_k + c] : 0.f;
+  const float* q = static_cast<const float*>(p.q) + (size_t)hk * d_k;
+  const float* k = static_cast<const float*>(p.k) + (size_t)hk * d_k;
+  const float* v = static_cast<const float*>(p.v) + (size_t)h * d_v;
+  float* O = static_cast<float*>(p.O) + (size_t)h * d_v;
+  const size_t qk_row = (size_t)p.h_k * d_k, v_row = (size_t)p.h_v * d_v;
+  const int t_end = seg.t_begin + seg.len;
+
+  // Rows [t0, t0 + 64) of a tensor into a tile; zero behind the segment's end and the head's width.
+  auto load = [&](float* tile, const float* src, size_t row, int d, int t0) {
+    for (int e = tid; e < C * (D / 4); e += NT) {
+      const int t = e / (D / 4), c = 4 * (e % (D / 4));
+      const bool there = t0 + t < t_end && c < d;
+      copy16(tile + t * TS + c, there ? src + (size_t)(t0 + t) * row + c : src, there);
+    }
+  };
+  if (seg.len > 0) {
+    if (OUT) load(sm.Q, q, qk_row, d_k, seg.t_begin);
+    load(sm.K, k, qk_row, d_k, seg.t_begin);
+    load(sm.V, v, v_row, d_v, seg.t_begin);
   }
-  const Tin* q = static_cast<const Tin*>(p.q);
-  const Tin* k = static_cast<const Tin*>(p.k);
-  const Tin* v = static_cast<const Tin*>(p.v);
-  Tin* O = static_cast<Tin*>(p.O);
-  for (int t0 = t_begin; t0 < t_end; t0 += C) {
+  copies_commit();
+  for (int n = tid; n <= C; n += NT) sm.pw[n] = n ? expf((float)n * g) : 1.f;
+  float s[RI][JN];  // rows RI y + i, columns x + 16 j
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+      const int r = RI * y + i, c = x + 16 * j;
+      s[i][j] = state.S_in && r < d_v && c < d_k ? state.S_in[(size_t)r * d_k + c] : 0.f;
+    }
+  auto publish_state = [&]() {
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+      float* at = sm.St + (x + 16 * j) * TS + RI * y;
+#pragma unroll
+      for (int i = 0; i < RI; i += 4)
+        *reinterpret_cast<float4*>(at + i) = make_float4(s[i][j], s[i + 1][j], s[i + 2][j], s[i + 3][j]);
+    }
+  };
+  if (OUT) publish_state();
+
+  for (int t0 = seg.t_begin; t0 < t_end; t0 += C) {
     const int n = min(C, t_end - t0);
+    const bool more = t0 + C < t_end;
+    copies_wait();
     __syncthreads();
-    for (int e = tid; e < C * d_k; e += NT) {
-      const int t = e / d_k, c = e % d_k;
-      const size_t at = ((size_t)(t0 + t) * p.h_k + hk) * d_k + c;
-      sm.K[t * QS + c] = t < n ? load1(k + at) : 0.f;
-      if (p.write_O) sm.Q[t * QS + c] = t < n ? load1(q + at) : 0.f;
-    }
-    for (int e = tid; e < C * R; e += NT) {
-      const int t = e / R, r = e % R;
-      const float x = t < n && r0 + r < d_v ? load1(v + ((size_t)(t0 + t) * p.h_v + h) * d_v + r0 + r) : 0.f;
-      sm.V[t * VS + r] = x;
-      sm.W[t * VS + r] = t < n ? x * sm.pw[n - 1 - t] : 0.f;
-    }
-    __syncthreads();
-    if (p.write_O) {
-      {  // P: rows ty + 16 a, columns tx + 16 b
+    if (OUT) {
+      {  // P: rows y + 16 a, columns x + 16 b; a block with b > a lies above the diagonal
         float acc[4][4] = {};
+#pragma unroll 2
         for (int c = 0; c < d_k; c += 4) {
-          float4 x[4], y[4];
+          float4 a4[4], b4[4];
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
-            x[a] = *reinterpret_cast<const float4*>(&sm.Q[(ty + 16 * a) * QS + c]);
-            y[a] = *reinterpret_cast<const float4*>(&sm.K[(tx + 16 * a) * QS + c]);
+            a4[a] = *reinterpret_cast<const float4*>(&sm.Q[(y + 16 * a) * TS + c]);
+            b4[a] = *reinterpret_cast<const float4*>(&sm.K[(x + 16 * a) * TS + c]);
           }
 #pragma unroll
           for (int a = 0; a < 4; ++a)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) acc[a][b] = dot4(x[a], y[b], acc[a][b]);
+            for (int b = 0; b <= a; ++b) acc[a][b] = dot4(a4[a], b4[b], acc[a][b]);
         }
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const int t = ty + 16 * a, s = tx + 16 * b;
-            sm.P[t * PS + s] = s <= t ? acc[a][b] * sm.pw[t - s] : 0.f;
+            const int t = y + 16 * a, e = x + 16 * b;
+            sm.P[t * PS + e] = e <= t ? acc[a][b] * sm.pw[t - e] : 0.f;
           }
       }
       __syncthreads();
-      {  // O: rows ty + 16 a, value columns tx + 16 b
-        float inter[4][2] = {}, intra[4][2] = {};
+      {  // O: rows row0 + i, columns col0 + [0, 4)
+        const int row0 = 8 * warp + (RI == 4 ? 4 * (lane >> 4) : 0), col0 = 4 * (RI == 4 ? lane & 15 : lane);
+        float4 o[RI];
+#pragma unroll
+        for (int i = 0; i < RI; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto rank1 = [&](float a, float4 b, float4& c) {
+          c = make_float4(fmaf(a, b.x, c.x), fmaf(a, b.y, c.y), fmaf(a, b.z, c.z), fmaf(a, b.w, c.w));
+        };
+#pragma unroll 2
         for (int c = 0; c < d_k; c += 4) {
-          float4 x[4], y[2];
+          float4 b[4];
 #pragma unroll
-          for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4*>(&sm.Q[(ty + 16 * a) * QS + c]);
+          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4*>(&sm.St[(c + e) * TS + col0]);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) y[b] = *reinterpret_cast<const float4*>(&sm.S[(tx + 16 * b) * QS + c]);
-#pragma unroll
-          for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) inter[a][b] = dot4(x[a], y[b], inter[a][b]);
-        }
-        for (int s = 0; s < C; ++s) {
-          const float y0 = sm.V[s * VS + tx], y1 = sm.V[s * VS + tx + 16];
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const float x = sm.P[(ty + 16 * a) * PS + s];
-            intra[a][0] = fmaf(x, y0, intra[a][0]);
-            intra[a][1] = fmaf(x, y1, intra[a][1]);
+          for (int i = 0; i < RI; ++i) {
+            const float4 a = *reinterpret_cast<const float4*>(&sm.Q[(row0 + i) * TS + c]);
+            rank1(a.x, b[0], o[i]);
+            rank1(a.y, b[1], o[i]);
+            rank1(a.z, b[2], o[i]);
+            rank1(a.w, b[3], o[i]);
           }
         }
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int i = 0; i < RI; ++i) {
+          const float f = sm.pw[row0 + i + 1];
+          o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
+        }
+#pragma unroll 2
+        for (int e0 = 0; e0 < 8 * warp + 8; e0 += 4) {  // (no later token counts for these rows)
+          float4 b[4];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int t = ty + 16 * a, r = r0 + tx + 16 * b;
-            if (t < n && r < d_v)
-              store1(O + ((size_t)(t0 + t) * p.h_v + h) * d_v + r,
-                     p.scale * fmaf(sm.pw[t + 1], inter[a][b], intra[a][b]));
-          }
-      }
-      __syncthreads();  // every reader of S is done
-    }
-    {  // S: rows (tid >> 5) + 8 a, columns 4 (tid & 31) + [0, 4)
-      const int c = 4 * (tid & 31), rr = tid >> 5;
-      if (c < d_k) {
-        float4 acc[4];
+          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4*>(&sm.V[(e0 + e) * TS + col0]);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) acc[a] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < n; ++s) {
-          const float4 y = *reinterpret_cast<const float4*>(&sm.K[s * QS + c]);
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const float x = sm.W[s * VS + rr + 8 * a];
-            acc[a].x = fmaf(x, y.x, acc[a].x);
-            acc[a].y = fmaf(x, y.y, acc[a].y);
-            acc[a].z = fmaf(x, y.z, acc[a].z);
-            acc[a].w = fmaf(x, y.w, acc[a].w);
+          for (int i = 0; i < RI; ++i) {
+            const float4 a = *reinterpret_cast<const float4*>(&sm.P[(row0 + i) * PS + e0]);
+            rank1(a.x, b[0], o[i]);
+            rank1(a.y, b[1], o[i]);
+            rank1(a.z, b[2], o[i]);
+            rank1(a.w, b[3], o[i]);
           }
         }
-        const DecayStep f = decay_step(g, n);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          float4* s = reinterpret_cast<float4*>(&sm.S[(rr + 8 * a) * QS + c]);
-          *s = make_float4(f(s->x, acc[a].x), f(s->y, acc[a].y), f(s->z, acc[a].z), f(s->w, acc[a].w));
+        for (int i = 0; i < RI; ++i) {
+          const int t = row0 + i;
+          if (t < n && col0 < d_v)
+            *reinterpret_cast<float4*>(O + (size_t)(t0 + t) * v_row + col0) =
+                make_float4(p.scale * o[i].x, p.scale * o[i].y, p.scale * o[i].z, p.scale * o[i].w);
         }
       }
+      __syncthreads();  // Q and the state's copy are read
+      if (more) load(sm.Q, q, qk_row, d_k, t0 + C);
+    }
+    {  // S
+      float acc[RI][JN] = {};
+#pragma unroll 2
+      for (int e = 0; e < n; ++e) {
+        const float w = sm.pw[n - 1 - e];
+        float a[RI];
+#pragma unroll
+        for (int i = 0; i < RI; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.V[e * TS + RI * y + i]);
+          a[i] = w * f.x; a[i + 1] = w * f.y; a[i + 2] = w * f.z; a[i + 3] = w * f.w;
+        }
+        float b[JN];
+#pragma unroll
+        for (int j = 0; j < JN; ++j) b[j] = sm.K[e * TS + x + 16 * j];
+#pragma unroll
+        for (int i = 0; i < RI; ++i)
+#pragma unroll
+          for (int j = 0; j < JN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      }
+      const DecayStep f = decay_step(g, n);
+#pragma unroll
+      for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < JN; ++j) s[i][j] = f(s[i][j], acc[i][j]);
+    }
+    if (more) {
+      if (OUT) publish_state();
+      __syncthreads();  // K and V are read
+      load(sm.K, k, qk_row, d_k, t0 + C);
+      load(sm.V, v, v_row, d_v, t0 + C);
+      copies_commit();
     }
   }
-  __syncthreads();
-  for (int e = tid; e < R * d_k; e += NT) {
-    const int r = e / d_k, c = e % d_k;
-    if (r0 + r < d_v) S_out[(size_t)(r0 + r) * d_k + c] = sm.S[r * QS + c];
-  }
+  if (state.dst < 0) return;
+  float* dst = (state.to_local ? p.local : p.S_out) + (size_t)state.dst * d_v * d_k;
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+      const int r = RI * y + i, c = x + 16 * j;
+      if (r < d_v && c < d_k) dst[(size_t)r * d_k + c] = s[i][j];
+    }
+}
+
+template <bool OUT, int JN, int RI>
+cudaError_t launch_items(const LinearWork& p, int units, cudaStream_t stream) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(linear_simt_kernel<OUT, JN, RI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)units * p.h_v);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = sizeof(Smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.behind_plan ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, linear_simt_kernel<OUT, JN, RI>, p);
+}
+
+template <bool OUT, int RI>
+cudaError_t launch_columns(const LinearWork& p, int units, cudaStream_t stream) {
+  if (p.d_k <= 64) return launch_items<OUT, 4, RI>(p, units, stream);
+  if (p.d_k <= 96) return launch_items<OUT, 6, RI>(p, units, stream);
+  return launch_items<OUT, 8, RI>(p, units, stream);
+}
+
+template <bool OUT>
+cudaError_t launch_shape(const LinearWork& p, int units, cudaStream_t stream) {
+  return p.d_v <= 64 ? launch_columns<OUT, 4>(p, units, stream) : launch_columns<OUT, 8>(p, units, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_simt(const LinearParams& p, int bf16, cudaStream_t stream) {
-  auto kern = bf16 ? linear_simt_kernel<__nv_bfloat16> : linear_simt_kernel<float>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-  if (e != cudaSuccess) return e;
-  const dim3 grid(p.n_seqs, p.h_v, (p.d_v + R - 1) / R);
-  kern<<<grid, NT, sizeof(Smem), stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_linear_simt_items(const LinearWork& p, bool out, int units, cudaStream_t stream) {
+  return out ? launch_shape<true>(p, units, stream) : launch_shape<false>(p, units, stream);
 }
 
 }  // namespace gdn

@@ -35,22 +35,15 @@
 //         stage of V that they replace, one fetches the work
 // Every hand-off is an mbarrier; every wait is bounded.
 //
-// A sequence longer than `seg_tokens` is cut into segments, so that a few long prompts fill the GPU:
-// the segments' own states first (KV only, from zero), then their entering states
-// (linear_carry_kernel), then every segment as above.
-//
 // One CTA per SM stays and takes item after item (clusterlaunchcontrol): the loads, products and tables
-// of the next item start while the last chunks of the one before are finished.  With several sequences
-// linear_plan_kernel lists the segments, longest first, once per call.
+// of the next item start while the last chunks of the one before are finished.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
-#include <algorithm>
 #include <atomic>
-#include <climits>
 
-#include "gdn_internal.cuh"
+#include "linear_work.cuh"
 #include "tc_common.cuh"
 
 namespace gdn {
@@ -109,146 +102,6 @@ enum Bar { kFull = 0, kEmpty = 3, kAFull = 6, kAFree = 10, kKV = 14, kKVFree = 1
            kSFull, kSFree, kVRead, kStaged = kVRead + 2, kFix = kStaged + 2, kDrainA = kFix + 2, kDrainB, kCorner, kSteal, kItem, kItemFree = kItem + 2,
            kPair = kItemFree + 2 /* one per quad */, kBars = kPair + 4 };
 static_assert(kBars <= 48, "barrier area");
-
-// One entry of the plan: a segment of a sequence.  seq < 0: none.
-struct Segment {
-  int seq, seg, n_seg, t_begin, len, local, pad0, pad1;
-};
-// The entering states of a cut sequence's segments are found sequence by sequence.
-struct CutSeq {
-  int seq, n_seg, local, last_len;
-};
-
-struct TcParams {
-  const float* log_decay;
-  const int32_t* cu;
-  const float* S0;
-  float* local;  // [cut segments][h_v][d_v][d_k]: the segments' own, then entering states
-  const Segment* list;  // the launch's items, or null: one sequence, segments in order
-  const CutSeq* cuts;   // linear_carry_kernel: cut sequences, or null: one sequence
-  __nv_bfloat16* O;
-  float* S_out;
-  int* status;
-  int n_seqs, total_tokens, h_k, h_v, d_k, d_v;
-  int seg_tokens;  // INT_MAX: sequences are not cut
-  int local_only;  // the segments' own states for a launch with outputs: the last one is not needed
-  float scale;
-};
-
-__device__ __forceinline__ int segments_of(int len, int seg_tokens) {
-  return len <= seg_tokens ? 1 : (len - 1) / seg_tokens + 1;
-}
-// Segment `u` of a call with one sequence (seq = -1: there is no such segment).
-__device__ __forceinline__ Segment only_segment(const TcParams& p, int u) {
-  Segment s = {};
-  const int a = p.cu[0], b = p.cu[1];
-  s.seq = -1;
-  if (a >= 0 && b >= a && b <= p.total_tokens) {
-    s.n_seg = segments_of(b - a, p.seg_tokens);
-    if (u < s.n_seg) {
-      s.seq = 0;
-      s.seg = s.local = u;
-      s.t_begin = a + u * (s.n_seg > 1 ? p.seg_tokens : 0);
-      s.len = min(p.seg_tokens, b - s.t_begin);
-    }
-  }
-  return s;
-}
-
-// The plan of a call with several sequences, one CTA: `units` entries, the segments of every sequence
-// with a valid range (longest first while they are at most kSortMost, else in order), then -1; `cut`
-// entries of the segments of cut sequences alone; `cuts` entries of the cut sequences.  A range
-// [cu[i], cu[i+1]) counts when 0 <= cu[i] <= cu[i+1] <= total_tokens and no earlier offset is above
-// cu[i]; others are reported.  An empty sequence is one segment of no tokens.
-constexpr int kPlanNT = 1024, kSortMost = 1024;
-__global__ void __launch_bounds__(kPlanNT) linear_plan_kernel(const int32_t* cu, int n_seqs, int total, int seg_tokens,
-                                                              Segment* list, int units, Segment* cut_list, int cut_units,
-                                                              CutSeq* cuts, int n_cuts, int* status) {
-  __shared__ int w_max[32], w_units[32], w_cut[32], w_cuts[32];
-  __shared__ int key[kSortMost];
-  grid_dep_launch();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < units; i += kPlanNT) list[i].seq = -1;
-  for (int i = tid; i < cut_units; i += kPlanNT) cut_list[i].seq = -1;
-  for (int i = tid; i < n_cuts; i += kPlanNT) cuts[i].seq = -1;
-  const bool sort = units <= kSortMost;
-  if (sort)
-    for (int i = tid; i < units; i += kPlanNT) key[i] = -1;
-  int c_max = INT_MIN, c_units = 0, c_cut = 0, c_cuts = 0;
-  __syncthreads();
-  for (int base = 0; base < n_seqs; base += kPlanNT) {
-    const int i = base + tid;
-    int a = 0, b = INT_MIN, top = INT_MIN;
-    if (i < n_seqs) {
-      a = cu[i];
-      b = cu[i + 1];
-      top = max(a, b);
-    }
-    int incl = top;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl = max(incl, x);
-    }
-    int before = __shfl_up_sync(0xffffffffu, incl, 1);
-    if (lane == 0) before = INT_MIN;
-    if (lane == 31) w_max[warp] = incl;
-    __syncthreads();
-    int all = c_max;
-    before = max(before, c_max);
-    for (int w = 0; w < kPlanNT / 32; ++w) {
-      if (w < warp) before = max(before, w_max[w]);
-      all = max(all, w_max[w]);
-    }
-    const bool ok = i < n_seqs && a >= 0 && a >= before && b >= a && b <= total;
-    if (i < n_seqs && !ok) atomicExch(status, GDN_ERR_SHAPE);
-    const int n = ok ? segments_of(b - a, seg_tokens) : 0;
-    // inclusive sums of segments, segments of cut sequences, cut sequences
-    int su = n, sc = n > 1 ? n : 0, sq = n > 1 ? 1 : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int xu = __shfl_up_sync(0xffffffffu, su, o), xc = __shfl_up_sync(0xffffffffu, sc, o),
-                xq = __shfl_up_sync(0xffffffffu, sq, o);
-      if (lane >= o) { su += xu; sc += xc; sq += xq; }
-    }
-    if (lane == 31) { w_units[warp] = su; w_cut[warp] = sc; w_cuts[warp] = sq; }
-    __syncthreads();
-    int bu = c_units, bc = c_cut, bq = c_cuts;
-    for (int w = 0; w < kPlanNT / 32; ++w) {
-      if (w < warp) { bu += w_units[w]; bc += w_cut[w]; bq += w_cuts[w]; }
-      c_units += w_units[w];
-      c_cut += w_cut[w];
-      c_cuts += w_cuts[w];
-    }
-    c_max = all;
-    bu += su - n;
-    bc += sc - (n > 1 ? n : 0);
-    bq += sq - (n > 1 ? 1 : 0);
-    for (int j = 0; j < n; ++j) {
-      Segment s = {};
-      s.seq = i; s.seg = j; s.n_seg = n; s.t_begin = a + j * (n > 1 ? seg_tokens : 0);
-      s.len = min(seg_tokens, b - s.t_begin); s.local = n > 1 ? bc + j : 0;
-      if (bu + j < units) {
-        list[bu + j] = s;
-        if (sort) key[bu + j] = s.len;
-      }
-      if (n > 1 && bc + j < cut_units) cut_list[bc + j] = s;
-    }
-    if (n > 1 && bq < n_cuts) cuts[bq] = CutSeq{i, n, bc, b - (a + (n - 1) * seg_tokens)};
-    __syncthreads();
-  }
-  if (!sort) return;
-  const int u = tid;
-  Segment s = {};
-  int rank = 0;
-  const bool have = u < units && key[u] >= 0;
-  if (have) {
-    s = list[u];
-    for (int j = 0; j < units; ++j) rank += key[j] > s.len || (key[j] == s.len && j < u);
-  }
-  __syncthreads();
-  if (have) list[rank] = s;
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -381,7 +234,7 @@ __global__ void __launch_bounds__(NT, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                      const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_local,
-                     const TcParams p) {
+                     const LinearWork p) {
   using L = Lay<OUT>;
   using TM = Tmem<OUT>;
   constexpr int kStages = L::kStages;
@@ -394,7 +247,6 @@ __global__ void __launch_bounds__(NT, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2, quad = warp & 3;
   const int dkp = p.d_k <= 64 ? 64 : 128, dvp = p.d_v <= 64 ? 64 : 128;  // columns that the products cover
-  const size_t dd = (size_t)p.d_v * p.d_k;
 
   if (smem_u32(sm) & 1023u) {  // (the swizzled tiles could not be addressed)
     if (tid == 0) atomicExch(p.status, GDN_ERR_CUDA);
@@ -566,7 +418,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (n < C && 8 * (lane & 7) + 64 * group < p.d_v) {
           const int col = 64 * group + 8 * (lane & 7);
           for (int row = 32 * quad + (lane >> 3); row < min(n, 32 * quad + 32); row += 4)
-            *reinterpret_cast<uint4*>(p.O + ((size_t)(t_begin + c * C + row) * p.h_v + h) * p.d_v + col) =
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + ((size_t)(t_begin + c * C + row) * p.h_v + h) * p.d_v + col) =
                 *reinterpret_cast<const uint4*>(stage + kbf16(row, col, 128));
         }
         fence_async_smem();
@@ -1002,18 +854,16 @@ __global__ void __launch_bounds__(NT, 1)
           }
           if (lane == 0) {
             Item* it = reinterpret_cast<Item*>(sm + L::ITEM + 64 * (k & 1));
-            const size_t whole = ((size_t)s.seq * p.h_v + h) * dd, part = ((size_t)s.local * p.h_v + h) * dd;
-            const bool cut = s.n_seg > 1;
+            const ItemState state = item_state(p, s, h, OUT);
             it->n_chunks = (s.len + C - 1) / C;
             it->t_begin = s.t_begin;
             it->n_last = s.len > 0 ? (s.len - 1) % C + 1 : C;
             it->h = h;
             it->g = g;
-            it->S_in = cut ? (OUT ? p.local + part : nullptr) : p.S0 ? p.S0 + whole : nullptr;
-            const bool final = !cut || (OUT && s.seg + 1 == s.n_seg);
-            it->to_local = !final;
-            it->dst = final ? s.seq * p.h_v + h : OUT ? -1 : s.local * p.h_v + h;
-            if (it->S_in) bulk_prefetch_l2(it->S_in, (uint32_t)(dd * 4));
+            it->S_in = state.S_in;
+            it->to_local = state.to_local;
+            it->dst = state.dst;
+            if (it->S_in) bulk_prefetch_l2(it->S_in, (uint32_t)(p.d_v * p.d_k * 4));
           }
           arrive(kItem + (k & 1));
           ++k;
@@ -1045,45 +895,6 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// The entering states of a cut sequence's segments, in place of the segments' own states, and (FINAL)
-// the state behind the last one.  Element by element: E <- lambda^seg E + local.
-constexpr int kCarryNT = 256;
-template <bool FINAL>
-__global__ void __launch_bounds__(kCarryNT) linear_carry_kernel(const TcParams p) {
-  const int h = blockIdx.x % p.h_v, i = blockIdx.x / p.h_v;
-  CutSeq q = {};
-  if (p.cuts) {
-    q = p.cuts[i];
-  } else {
-    const Segment s = only_segment(p, 0);
-    q.seq = s.seq;
-    q.n_seg = s.n_seg;
-    q.last_len = s.seq < 0 ? 0 : p.cu[1] - (p.cu[0] + (s.n_seg - 1) * p.seg_tokens);
-  }
-  if (q.seq < 0 || q.n_seg < 2) return;
-  const float g = p.log_decay[h];
-  const int dd = p.d_v * p.d_k;
-  const int e = (blockIdx.y * kCarryNT + threadIdx.x) * 4;
-  if (e >= dd) return;
-  const size_t at = ((size_t)q.seq * p.h_v + h) * dd + e;
-  float4 E = p.S0 ? *reinterpret_cast<const float4*>(p.S0 + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const DecayStep step = decay_step(g, p.seg_tokens);
-  const size_t stride = (size_t)p.h_v * dd;
-  float* loc = p.local + ((size_t)q.local * p.h_v + h) * dd + e;
-  for (int j = 0; j < q.n_seg; ++j, loc += stride) {
-    const bool last = j + 1 == q.n_seg;
-    if (FINAL || !last) {
-      const float4 x = *reinterpret_cast<const float4*>(loc);
-      if (!FINAL) *reinterpret_cast<float4*>(loc) = E;
-      const DecayStep f = last ? decay_step(g, q.last_len) : step;
-      E = make_float4(f(E.x, x.x), f(E.y, x.y), f(E.z, x.z), f(E.w, x.w));
-    } else {
-      *reinterpret_cast<float4*>(loc) = E;
-    }
-  }
-  if (FINAL) *reinterpret_cast<float4*>(p.S_out + at) = E;
-}
-
 // [T][heads][d] as a 3-D tensor, boxes of 64 elements x one head x 128 tokens; elements past d and
 // tokens past T read as zero.
 bool make_map_heads(CUtensorMap* m, const void* base, int tokens, int heads, int d) {
@@ -1111,22 +922,16 @@ bool make_map_states(CUtensorMap* m, const void* base, size_t count, int d_v, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMinSegment = 512;
-
-// What the launches need to know of a device, looked up once: its SMs, and that the kernels may have
-// their shared memory and are launched with the registers that the warpgroups' shares add up to (with
-// fewer, a warpgroup that asks for more would wait).
-cudaError_t prepare_device(int* sms) {
+// The kernels may have their shared memory, and are launched with the registers that the warpgroups'
+// shares add up to (with fewer, a warpgroup that asks for more would wait): checked once per device.
+cudaError_t prepare_device() {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices];
+  static std::atomic<bool> ready[kDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
-  *sms = known[dev].load(std::memory_order_acquire);
-  if (*sms > 0) return cudaSuccess;
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
   const void* kernels[] = {reinterpret_cast<const void*>(linear_tc_kernel<true>),
                            reinterpret_cast<const void*>(linear_tc_kernel<false>)};
   const int bytes[] = {(int)Lay<true>::TOTAL, (int)Lay<false>::TOTAL};
@@ -1138,54 +943,22 @@ cudaError_t prepare_device(int* sms) {
     e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]);
     if (e != cudaSuccess) return e;
   }
-  known[dev].store(*sms, std::memory_order_release);
+  ready[dev].store(true, std::memory_order_release);
   return cudaSuccess;
 }
 
-// Tokens per segment: one sequence's segments times the v-heads fill the GPU once.
-int segment_tokens(int total_tokens, int h_v, int sms) {
-  const int parts = std::max(1, sms / h_v);
-  const int seg = ((total_tokens + parts - 1) / parts + C - 1) / C * C;
-  return seg >= total_tokens ? INT_MAX : std::max(seg, kMinSegment);
-}
-
-// What a call keeps in its workspace: the plan's lists (none for one sequence), the cut segments' states.
-struct Workspace {
-  int seg, units, cut_units, cuts;
-  size_t list, cut_list, cut_seqs, local, bytes;
-};
-Workspace workspace_of(const LinearParams& p, int sms) {
-  Workspace w = {};
-  const int seg = segment_tokens(p.total_tokens, p.h_v, sms);
-  const bool cut = seg < p.total_tokens;
-  w.seg = cut ? seg : INT_MAX;
-  // sum of max(1, ceil(len / seg)) <= n + total / seg; a cut sequence is longer than seg
-  w.cuts = cut ? std::min(p.n_seqs, p.total_tokens / seg) : 0;
-  w.cut_units = cut ? w.cuts + p.total_tokens / seg : 0;
-  w.units = p.n_seqs + (cut ? p.total_tokens / seg : 0);
-  size_t at = 0;
-  auto take = [&](size_t bytes) {
-    const size_t here = at;
-    at += (bytes + 255) / 256 * 256;
-    return here;
-  };
-  if (p.n_seqs > 1) {
-    w.list = take(sizeof(Segment) * (size_t)w.units);
-    w.cut_list = take(sizeof(Segment) * (size_t)w.cut_units);
-    w.cut_seqs = take(sizeof(CutSeq) * (size_t)w.cuts);
-  }
-  w.local = take((size_t)w.cut_units * p.h_v * p.d_v * p.d_k * 4);
-  w.bytes = at;
-  return w;
-}
-
 template <bool OUT>
-cudaError_t launch_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
-                         const CUtensorMap& ms, const CUtensorMap& ml, const TcParams& p, int units, bool behind_plan, cudaStream_t stream) {
-  const long long blocks = (long long)units * p.h_v;
-  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+cudaError_t launch_items(const LinearWork& p, int units, cudaStream_t stream) {
+  CUtensorMap mq{}, mk, mv, mo{}, ms, ml{};
+  if ((OUT && (!make_map_heads(&mq, p.q, p.total_tokens, p.h_k, p.d_k) ||
+               !make_map_heads(&mo, p.O, p.total_tokens, p.h_v, p.d_v))) ||
+      !make_map_heads(&mk, p.k, p.total_tokens, p.h_k, p.d_k) ||
+      !make_map_heads(&mv, p.v, p.total_tokens, p.h_v, p.d_v) ||
+      !make_map_states(&ms, p.S_out, (size_t)p.n_seqs * p.h_v, p.d_v, p.d_k) ||
+      (p.cut_units > 0 && !make_map_states(&ml, p.local, (size_t)p.cut_units * p.h_v, p.d_v, p.d_k)))
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)units * p.h_v);
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = Lay<OUT>::TOTAL;
   cfg.stream = stream;
@@ -1193,72 +966,16 @@ cudaError_t launch_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = behind_plan ? 1 : 0;
+  cfg.numAttrs = p.behind_plan ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, linear_tc_kernel<OUT>, mq, mk, mv, mo, ms, ml, p);
 }
 
 }  // namespace
 
-bool linear_tc_supported(const LinearParams& p) { return p.total_tokens > 0; }
-
-cudaError_t linear_tc_workspace_bytes(const LinearParams& p, size_t* bytes) {
-  int sms = 0;
-  const cudaError_t e = prepare_device(&sms);
-  if (e == cudaSuccess) *bytes = workspace_of(p, sms).bytes;
-  return e;
-}
-
-cudaError_t launch_linear_tc(const LinearParams& lp, void* workspace, cudaStream_t stream) {
-  int sms = 0;
-  cudaError_t e = prepare_device(&sms);
+cudaError_t launch_linear_tc_items(const LinearWork& p, bool out, int units, cudaStream_t stream) {
+  const cudaError_t e = prepare_device();
   if (e != cudaSuccess) return e;
-  CUtensorMap mq{}, mk, mv, mo{}, ms, ml{};
-  if ((lp.write_O && (!make_map_heads(&mq, lp.q, lp.total_tokens, lp.h_k, lp.d_k) ||
-                      !make_map_heads(&mo, lp.O, lp.total_tokens, lp.h_v, lp.d_v))) ||
-      !make_map_heads(&mk, lp.k, lp.total_tokens, lp.h_k, lp.d_k) ||
-      !make_map_heads(&mv, lp.v, lp.total_tokens, lp.h_v, lp.d_v))
-    return cudaErrorInvalidValue;
-  const Workspace w = workspace_of(lp, sms);
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
-  if (!make_map_states(&ms, lp.S_out, (size_t)lp.n_seqs * lp.h_v, lp.d_v, lp.d_k) ||
-      (w.cut_units > 0 && !make_map_states(&ml, ws + w.local, (size_t)w.cut_units * lp.h_v, lp.d_v, lp.d_k)))
-    return cudaErrorInvalidValue;
-  TcParams p{};
-  p.log_decay = lp.log_decay; p.cu = lp.cu; p.S0 = lp.S0; p.local = reinterpret_cast<float*>(ws + w.local);
-  p.O = static_cast<__nv_bfloat16*>(lp.O); p.S_out = lp.S_out; p.status = lp.status;
-  p.n_seqs = lp.n_seqs; p.total_tokens = lp.total_tokens; p.h_k = lp.h_k; p.h_v = lp.h_v; p.d_k = lp.d_k; p.d_v = lp.d_v;
-  p.scale = lp.scale;
-  p.seg_tokens = w.seg;
-  const bool cut = w.cuts > 0, plan = lp.n_seqs > 1;
-  Segment* list = plan ? reinterpret_cast<Segment*>(ws + w.list) : nullptr;
-  Segment* cut_list = plan ? reinterpret_cast<Segment*>(ws + w.cut_list) : nullptr;
-  CutSeq* cuts = plan ? reinterpret_cast<CutSeq*>(ws + w.cut_seqs) : nullptr;
-  if (plan) {
-    linear_plan_kernel<<<1, kPlanNT, 0, stream>>>(lp.cu, lp.n_seqs, lp.total_tokens, w.seg, list, w.units, cut_list,
-                                                  w.cut_units, cuts, w.cuts, lp.status);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  p.list = list;
-  p.cuts = cuts;
-  if (!lp.write_O) {
-    e = launch_items<false>(mq, mk, mv, mo, ms, ml, p, w.units, plan, stream);
-  } else if (cut) {
-    TcParams own = p;
-    own.list = cut_list;
-    own.local_only = 1;
-    e = launch_items<false>(mq, mk, mv, mo, ms, ml, own, w.cut_units, plan, stream);
-  }
-  if (e != cudaSuccess) return e;
-  if (cut) {
-    const dim3 grid((unsigned)(w.cuts * lp.h_v), (lp.d_v * lp.d_k / 4 + kCarryNT - 1) / kCarryNT);
-    if (lp.write_O) linear_carry_kernel<false><<<grid, kCarryNT, 0, stream>>>(p);
-    else linear_carry_kernel<true><<<grid, kCarryNT, 0, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (lp.write_O) e = launch_items<true>(mq, mk, mv, mo, ms, ml, p, w.units, plan && !cut, stream);
-  return e;
+  return out ? launch_items<true>(p, units, stream) : launch_items<false>(p, units, stream);
 }
 
 }  // namespace gdn
