@@ -112,6 +112,8 @@ constexpr int kCarryNT = 256, kAhead = 8;
 template <bool FINAL>
 __global__ void __launch_bounds__(kCarryNT) linear_carry_kernel(const LinearWork p) {
   const int h = blockIdx.x % p.h_v, i = blockIdx.x / p.h_v;
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();  // the segments' own states
   CutSeq q = {};
   if (p.cuts) {
     q = p.cuts[i];
@@ -248,25 +250,33 @@ cudaError_t launch_linear(const LinearParams& lp, int bf16, void* workspace, cud
   p.cuts = cuts;
   const auto items = tc ? launch_linear_tc_items : launch_linear_simt_items;
   if (!lp.write_O) {
-    p.behind_plan = plan;
+    p.early = plan;
     e = items(p, false, w.units, stream);
   } else if (cut) {
     LinearWork own = p;
     own.list = cut_list;
     own.local_only = 1;
-    own.behind_plan = plan;
+    own.early = plan;
     e = items(own, false, w.cut_units, stream);
   }
   if (e != cudaSuccess) return e;
   if (cut) {
     const dim3 grid((unsigned)(w.cuts * lp.h_v), (lp.d_v * lp.d_k / 4 + kCarryNT - 1) / kCarryNT);
-    if (lp.write_O) linear_carry_kernel<false><<<grid, kCarryNT, 0, stream>>>(p);
-    else linear_carry_kernel<true><<<grid, kCarryNT, 0, stream>>>(p);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kCarryNT);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = lp.write_O ? cudaLaunchKernelEx(&cfg, linear_carry_kernel<false>, p)
+                   : cudaLaunchKernelEx(&cfg, linear_carry_kernel<true>, p);
     if (e != cudaSuccess) return e;
   }
   if (!lp.write_O) return cudaSuccess;
-  p.behind_plan = plan && !cut;
+  p.early = plan || cut;
   return items(p, true, w.units, stream);
 }
 

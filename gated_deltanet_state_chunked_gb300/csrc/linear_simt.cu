@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = tid & 15, y = tid >> 4;
   const int h = blockIdx.x % p.h_v, u = blockIdx.x / p.h_v;
+  tc::grid_dep_launch();
   if (p.list) tc::grid_dep_wait();  // the plan
   const Segment seg = p.list ? p.list[u] : only_segment(p, u);
   if (!p.list && blockIdx.x == 0 && tid == 0 && seg.seq < 0) atomicExch(p.status, GDN_ERR_SHAPE);
@@ -75,6 +76,7 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
   }
   copies_commit();
   for (int n = tid; n <= C; n += NT) sm.pw[n] = n ? expf((float)n * g) : 1.f;
+  if (OUT && seg.n_seg > 1) tc::grid_dep_wait();  // the entering states
   float s[RI][JN];  // rows RI y + i, columns x + 16 j
 #pragma unroll
   for (int i = 0; i < RI; ++i)
@@ -234,7 +236,7 @@ cudaError_t launch_items(const LinearWork& p, int units, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.behind_plan ? 1 : 0;
+  cfg.numAttrs = p.early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, linear_simt_kernel<OUT, JN, RI>, p);
 }
 

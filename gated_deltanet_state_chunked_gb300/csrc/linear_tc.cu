@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(NT, 1)
     for (int k = 0, gc = 0, fixes = 0; ok && get_item(k); ++k) {
       const int n_chunks = item_at(k)->n_chunks, n_last = item_at(k)->n_last;
       if (const float* S_in = item_at(k)->S_in) {
+        if (OUT && p.early) grid_dep_wait();  // the entering states
         // (all loads under way at once: s holds them in the order of memory first)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -828,18 +829,11 @@ __global__ void __launch_bounds__(NT, 1)
       bool ok = true;
       if (p.list) grid_dep_wait();  // the plan
       for (int steals = 0; ok; ++steals) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bar[kSteal], 16);
-          steal_block(sm + L::STEAL, &bar[kSteal]);
-        }
         const int h = block % p.h_v, u = block / p.h_v;
         const Segment s = p.list ? p.list[u] : only_segment(p, u);
         if (!p.list && block == 0 && lane == 0 && s.seq < 0) atomicExch(p.status, GDN_ERR_SHAPE);
         if (s.seq >= 0 && !(p.local_only && s.seg + 1 == s.n_seg)) {
-          if (k >= 2 && !(ok = wait(kItemFree + (k & 1), (k >> 1) - 1, kItemNs))) {
-            mbar_wait(&bar[kSteal], (uint32_t)(steals & 1), kWaitNs);  // (its answer is written here)
-            break;
-          }
+          if (k >= 2 && !(ok = wait(kItemFree + (k & 1), (k >> 1) - 1, kItemNs))) break;
           const float g = p.log_decay[h];
           float* cf = reinterpret_cast<float*>(sm + L::CF + 128 * (k & 1));
           cf[lane] = lane == 31 ? 1.f : expf((float)(31 - lane) * g);
@@ -867,6 +861,12 @@ __global__ void __launch_bounds__(NT, 1)
           }
           arrive(kItem + (k & 1));
           ++k;
+        }
+        // (CTAs that were launched early take nothing from those that start when the kernel ahead ends)
+        if (p.early) grid_dep_wait();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar[kSteal], 16);
+          steal_block(sm + L::STEAL, &bar[kSteal]);
         }
         if (!(ok = wait(kSteal, steals))) break;
         if (!stolen_block(sm + L::STEAL, block)) break;
@@ -966,7 +966,7 @@ cudaError_t launch_items(const LinearWork& p, int units, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.behind_plan ? 1 : 0;
+  cfg.numAttrs = p.early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, linear_tc_kernel<OUT>, mq, mk, mv, mo, ms, ml, p);
 }
 

@@ -39,7 +39,8 @@ struct LinearWork {
   int seg_tokens;   // INT_MAX: sequences are not cut
   int cut_units;    // segments that `local` has room for
   int local_only;   // the segments' own states for a launch with outputs: the last one is not needed
-  int behind_plan;  // the launch directly behind the plan kernel: it may start early and waits for the list
+  int early;        // the launch may start before the kernel ahead of it ends, and waits for it before
+                    // it reads the list (where there is one) or a state in `local`
   float scale;
 };
 
