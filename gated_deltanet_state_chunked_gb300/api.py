@@ -199,20 +199,21 @@ def _cuda_index(name, t):
     return t.get_device()
 
 
-def _launch(call, where, device, stream, outputs, *args):
-    """Allocate the missing outputs ({name: (shape, dtype)} for None entries) and make the C call on
-    ``device`` and ``stream`` (None: the current one).  What is allocated here belongs to the stream that
-    the kernels run on."""
+def _launch(call, where, ref, stream, outputs, *args):
+    """Allocate the missing outputs, given as (shape, dtype), and make the C call on the device of the
+    tensor ``ref`` and on ``stream`` (None: the current one).  What is allocated here belongs to the
+    stream that the kernels run on.  Returns the outputs."""
+    device = ref.get_device()
     if stream is not None:
         if stream.device.index != device:
             raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{device}")
         if stream != torch.cuda.current_stream(device) or torch.cuda.current_device() != device:
             with torch.cuda.stream(stream):
-                return _launch(call, where, device, None, outputs, *args)
+                return _launch(call, where, ref, None, outputs, *args)
     elif torch.cuda.current_device() != device:
         with torch.cuda.device(device):
-            return _launch(call, where, device, None, outputs, *args)
-    made = [t if not isinstance(t, tuple) else torch.empty(t[0], dtype=t[1], device=f"cuda:{device}") for t in outputs]
+            return _launch(call, where, ref, None, outputs, *args)
+    made = [torch.empty(t[0], dtype=t[1], device=ref.device) if type(t) is tuple else t for t in outputs]
     rc = call(*args, *[None if t is None else t.data_ptr() for t in made], _raw_stream(device))
     if rc != _lib.GDN_OK:
         _lib.check(rc, where)
@@ -244,7 +245,7 @@ def gdn_linear_attn(q, k, v, log_decay, cu_seqlens, S0=None, *, O_out=None, S_ou
     _want("O_out", O_out, dev, dt, vo)
     _want("S_out", S_out, dev, torch.float32, state)
     dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], _lib.GDN_STATE_ONLY if state_only else 0, scale)
-    O, S = _launch(lib.gdn_linear_attn, "gdn_linear_attn", dev, stream,
+    O, S = _launch(lib.gdn_linear_attn, "gdn_linear_attn", k, stream,
                    (None if state_only else (vo, dt) if O_out is None else O_out,
                     (state, torch.float32) if S_out is None else S_out), dims, *args)
     return O, S
@@ -285,7 +286,7 @@ def gdn_decode(q, k, v, g, beta, S_pool, slots=None, *, counts=None, O_out=None,
         | (_lib.GDN_SCALAR_DECAY if scalar_decay else 0) | (_lib.GDN_HEAD_DECAY if head_decay else 0) \
         | (_lib.GDN_KEEP_STATE if keep_state else 0)
     dims = _lib.GdnDims(n, T, h_k, h_v, d_k, d_v, _DTYPE[dt], flags, scale)
-    return _launch(lib.gdn_decode, "gdn_decode", dev, stream,
+    return _launch(lib.gdn_decode, "gdn_decode", k, stream,
                    (None if state_only else (vo, dt) if O_out is None else O_out,), dims, *args)[0]
 
 
@@ -333,7 +334,7 @@ def gdn_verify_draft(target, drafted, uniforms, draft=None, draft_lens=None, *, 
     _want("counts_out", counts_out, dev, i32, (n,))
     _want("tokens_out", tokens_out, dev, i32, emitted)
     dims = _lib.GdnVerifyDims(n, n_draft, vocab, _DTYPE[dt], target_stride, draft_stride)
-    counts, tokens = _launch(lib.gdn_verify_draft, "gdn_verify_draft", dev, stream,
+    counts, tokens = _launch(lib.gdn_verify_draft, "gdn_verify_draft", target, stream,
                              (((n,), i32) if counts_out is None else counts_out,
                               (emitted, i32) if tokens_out is None else tokens_out), dims, *args)
     return counts, tokens

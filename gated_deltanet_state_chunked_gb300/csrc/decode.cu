@@ -270,6 +270,8 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t stream) {
 
 template <typename Tin, int J, int W>
 cudaError_t launch_rows(const DecodeParams& p, cudaStream_t stream) {
+  // Few states: 32 rows a CTA instead of 64, so that more SMs take part (one request of 32 heads, one
+  // token: 3.5 us against 4.4; four: 5.1 against 5.3; eight, 256 states: 9.7 against 8.8).
   const bool few = (long long)p.n * p.h_v < 152;
   if (p.family == kDelta) return few ? launch<Tin, J, W, 1, true>(p, stream) : launch<Tin, J, W, 2, true>(p, stream);
   return few ? launch<Tin, J, W, 1, false>(p, stream) : launch<Tin, J, W, 2, false>(p, stream);

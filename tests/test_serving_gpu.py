@@ -664,3 +664,97 @@ def test_speculative_step_without_the_host(family):
     _, after = ref.decode(x["q"], x["k"], x["v"], x["g"], x["beta"], x["S_pool"], slots.tolist(), got, w, family=family,
                           l2norm=family == "delta")
     assert _rel(pool.double().cpu(), after) <= 2e-6
+
+
+# ------------------------------------------------------------------ together with others, and again
+
+
+def test_prompt_many_short_sequences_beside_a_replay():
+    """Two hundred sequences from none to 300 tokens (work items of one chunk and of none follow each
+    other), beside a replay on another stream; every repetition gives the same bits."""
+    gen = _gen(101)
+    lens = torch.randint(0, 300, (200,), generator=gen).tolist()
+    lens[3:9] = [128, 1, 0, 0, 127, 129]
+    x = _prompt_inputs(lens, 1, 3, 128, 128, BF16, 102, True)
+    d = _cuda(x)
+    r = _prompt_inputs([900, 700], 2, 4, 128, 128, BF16, 103, False)
+    rd = _cuda(r)
+    g = -0.1 * torch.rand(1600, 4, generator=gen).cuda()
+    beta = torch.rand(1600, 4, generator=gen).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    runs, replays = [], []
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            replays.append(api.gdn_replay(rd["q"], rd["k"], rd["v"], g, beta, rd["cu_seqlens"]))
+        runs.append(api.gdn_linear_attn(**d))
+    torch.cuda.synchronize()
+    api.gdn_get_status()
+    for O, S in runs[1:]:
+        assert torch.equal(O, runs[0][0]) and torch.equal(S, runs[0][1])
+    for O, S in replays[1:]:
+        assert torch.equal(O, replays[0][0]) and torch.equal(S, replays[0][1])
+    _check_prompt(x, *runs[0])
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("lens", [[5000], [40, 3000, 0, 777, 2500, 1], [640] * 3])
+def test_prompt_cut_sequences(dt, lens):
+    """Few heads: sequences cut into segments, whole ones among them, ends inside chunks and on them."""
+    x = _prompt_inputs(lens, 1, 1, 64, 96, dt, 200 + len(lens), True)
+    d = _cuda(x)
+    O, S = api.gdn_linear_attn(**d)
+    _, S2 = api.gdn_linear_attn(**dict(d, q=None), state_only=True)
+    api.gdn_get_status()
+    _check_prompt(x, O, S)
+    _check_prompt(x, None, S2)
+
+
+@pytest.mark.parametrize("n,w", [(3, 17), (200, 9)])
+def test_decode_windows_longer_than_unrolled(n, w):
+    x = _decode_inputs(n, w, 1, 2, 128, 64, BF16, 300 + w, "delta", n)
+    d = _cuda(x)
+    counts = [(5 * i) % (w + 1) for i in range(n)]
+    O = torch.zeros(n * w, 2, 64, dtype=BF16, device="cuda")
+    api.gdn_decode(**d, counts=torch.tensor(counts, dtype=torch.int32, device="cuda"), O_out=O)
+    api.gdn_get_status()
+    _check_decode(x, w, O, d["S_pool"], counts=counts, before=torch.zeros(n * w, 2, 64, dtype=BF16))
+
+
+def test_decode_extreme_gates():
+    """Gates from none to a full wipe (alpha = 0), per token and per head."""
+    for family in ("delta", "scalar", "head"):
+        x = _decode_inputs(2, 4, 1, 3, 64, 64, F32, 400, family, 2)
+        if family == "head":
+            x["g"] = torch.tensor([0.0, -200.0, float("-inf")])
+        else:
+            x["g"][1] = float("-inf")
+            x["g"][2] = 0.0
+            x["g"][5] = -200.0
+        d = _cuda(x)
+        O = api.gdn_decode(**d, scalar_decay=family == "scalar", head_decay=family == "head")
+        api.gdn_get_status()
+        _check_decode(x, 4, O, d["S_pool"], family=family)
+
+
+def test_calls_on_another_stream_than_their_outputs():
+    """Outputs that a call allocates belong to the stream it runs on."""
+    side = torch.cuda.Stream()
+    x = _decode_inputs(2, 1, 1, 2, 128, 128, BF16, 500, "delta", 2)
+    d = _cuda(x)
+    target, draft, drafted, u = _verify_inputs(4, 3, 5000, F32, 501)
+    c = [t.cuda() for t in (target, drafted, u, draft)]
+    torch.cuda.synchronize()
+    O = api.gdn_decode(**d, stream=side)
+    counts, tokens = api.gdn_verify_draft(*c, stream=side)
+    side.synchronize()
+    _check_decode(x, 1, O, d["S_pool"])
+    assert (counts.tolist(), tokens.tolist()) == ref.verify(target, drafted, u, draft, [3] * 4)
+
+
+def test_verify_largest_vocabulary_and_many_requests():
+    target, draft, drafted, u = _verify_inputs(2, 2, 1 << 19, F32, 600)
+    _check_verify(target, drafted, u, draft, None)
+    target, draft, drafted, u = _verify_inputs(700, 2, 9000, BF16, 601)
+    _check_verify(target, drafted, u, draft, None)
+    _check_verify(target, drafted, u, None, None)
