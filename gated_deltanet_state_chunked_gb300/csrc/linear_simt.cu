@@ -23,12 +23,27 @@ constexpr int TS = D + 4;  // row stride (floats) of Q, K, V and of the state's 
 constexpr int PS = C + 4;
 
 struct Smem {
-  float Q[C * TS], K[C * TS], V[C * TS], St[D * TS], P[C * PS];
+  float Q[C * TS], KV[3][C * TS], St[D * TS], P[C * PS];  // KV: keys, values, and the next chunk's keys, by turns
   float pw[C + 1];  // lambda^n
 };
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+// Two fused multiply-adds in one instruction (values as register pairs): the same rate as two, but half
+// the issue slots, which the loads beside them need.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
 }
 // 16 bytes of global memory into shared memory, or zeros.
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
@@ -36,7 +51,9 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool there)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// All copies are there but those of the last `left` groups.
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // JN: groups of 16 state columns (d_k at most 16 JN); RI: state rows a thread (d_v at most 16 RI), 8 or 4,
 // and as many rows of O (at 4 a warp's halves take four rows each).
@@ -71,8 +88,9 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
   };
   if (seg.len > 0) {
     if (OUT) load(sm.Q, q, qk_row, d_k, seg.t_begin);
-    load(sm.K, k, qk_row, d_k, seg.t_begin);
-    load(sm.V, v, v_row, d_v, seg.t_begin);
+    load(sm.KV[0], k, qk_row, d_k, seg.t_begin);
+    copies_commit();
+    load(sm.KV[1], v, v_row, d_v, seg.t_begin);
   }
   copies_commit();
   for (int n = tid; n <= C; n += NT) sm.pw[n] = n ? expf((float)n * g) : 1.f;
@@ -96,11 +114,14 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
   };
   if (OUT) publish_state();
 
+  float *tk = sm.KV[0], *tv = sm.KV[1], *spare = sm.KV[2];
   for (int t0 = seg.t_begin; t0 < t_end; t0 += C) {
     const int n = min(C, t_end - t0);
     const bool more = t0 + C < t_end;
-    copies_wait();
+    copies_wait<1>();  // queries and keys (the values may still be on their way)
     __syncthreads();
+    if (more) load(spare, k, qk_row, d_k, t0 + C);
+    copies_commit();
     if (OUT) {
       {  // P: rows y + 16 a, columns x + 16 b; a block with b > a lies above the diagonal
         float acc[4][4] = {};
@@ -110,7 +131,7 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
             a4[a] = *reinterpret_cast<const float4*>(&sm.Q[(y + 16 * a) * TS + c]);
-            b4[a] = *reinterpret_cast<const float4*>(&sm.K[(x + 16 * a) * TS + c]);
+            b4[a] = *reinterpret_cast<const float4*>(&tk[(x + 16 * a) * TS + c]);
           }
 #pragma unroll
           for (int a = 0; a < 4; ++a)
@@ -125,20 +146,23 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
             sm.P[t * PS + e] = e <= t ? acc[a][b] * sm.pw[t - e] : 0.f;
           }
       }
+      copies_wait<1>();  // values (all but the next keys)
       __syncthreads();
       {  // O: rows row0 + i, columns col0 + [0, 4)
         const int row0 = 8 * warp + (RI == 4 ? 4 * (lane >> 4) : 0), col0 = 4 * (RI == 4 ? lane & 15 : lane);
-        float4 o[RI];
+        uint64_t o[RI][2];  // pairs of columns
 #pragma unroll
-        for (int i = 0; i < RI; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto rank1 = [&](float a, float4 b, float4& c) {
-          c = make_float4(fmaf(a, b.x, c.x), fmaf(a, b.y, c.y), fmaf(a, b.z, c.z), fmaf(a, b.w, c.w));
+        for (int i = 0; i < RI; ++i) o[i][0] = o[i][1] = 0;
+        auto rank1 = [&](float a, ulonglong2 b, uint64_t (&c)[2]) {
+          const uint64_t a2 = pair(a, a);
+          c[0] = fma2(a2, b.x, c[0]);
+          c[1] = fma2(a2, b.y, c[1]);
         };
 #pragma unroll 2
         for (int c = 0; c < d_k; c += 4) {
-          float4 b[4];
+          ulonglong2 b[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4*>(&sm.St[(c + e) * TS + col0]);
+          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const ulonglong2*>(&sm.St[(c + e) * TS + col0]);
 #pragma unroll
           for (int i = 0; i < RI; ++i) {
             const float4 a = *reinterpret_cast<const float4*>(&sm.Q[(row0 + i) * TS + c]);
@@ -151,13 +175,14 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
           const float f = sm.pw[row0 + i + 1];
-          o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) o[i][e] = fma2(pair(f, f), o[i][e], 0);
         }
 #pragma unroll 2
         for (int e0 = 0; e0 < 8 * warp + 8; e0 += 4) {  // (no later token counts for these rows)
-          float4 b[4];
+          ulonglong2 b[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4*>(&sm.V[(e0 + e) * TS + col0]);
+          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const ulonglong2*>(&tv[(e0 + e) * TS + col0]);
 #pragma unroll
           for (int i = 0; i < RI; ++i) {
             const float4 a = *reinterpret_cast<const float4*>(&sm.P[(row0 + i) * PS + e0]);
@@ -170,45 +195,67 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
           const int t = row0 + i;
+          float a, b, c, d;
+          unpair(o[i][0], a, b);
+          unpair(o[i][1], c, d);
           if (t < n && col0 < d_v)
             *reinterpret_cast<float4*>(O + (size_t)(t0 + t) * v_row + col0) =
-                make_float4(p.scale * o[i].x, p.scale * o[i].y, p.scale * o[i].z, p.scale * o[i].w);
+                make_float4(p.scale * a, p.scale * b, p.scale * c, p.scale * d);
         }
       }
       __syncthreads();  // Q and the state's copy are read
       if (more) load(sm.Q, q, qk_row, d_k, t0 + C);
+    } else {
+      copies_wait<1>();
+      __syncthreads();
     }
+    copies_commit();
+    // the values times their weights, in place
+    for (int e = tid; e < n * (D / 4); e += NT) {
+      float4* at = reinterpret_cast<float4*>(&tv[e / (D / 4) * TS + 4 * (e % (D / 4))]);
+      const float w = sm.pw[n - 1 - e / (D / 4)];
+      *at = make_float4(w * at->x, w * at->y, w * at->z, w * at->w);
+    }
+    __syncthreads();
     {  // S
-      float acc[RI][JN] = {};
-#pragma unroll 2
+      uint64_t acc[RI / 2][JN] = {};  // pairs of rows
+#pragma unroll 4
       for (int e = 0; e < n; ++e) {
-        const float w = sm.pw[n - 1 - e];
-        float a[RI];
+        uint64_t a[RI / 2];
 #pragma unroll
         for (int i = 0; i < RI; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.V[e * TS + RI * y + i]);
-          a[i] = w * f.x; a[i + 1] = w * f.y; a[i + 2] = w * f.z; a[i + 3] = w * f.w;
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&tv[e * TS + RI * y + i]);
+          a[i / 2] = f.x;
+          a[i / 2 + 1] = f.y;
         }
-        float b[JN];
 #pragma unroll
-        for (int j = 0; j < JN; ++j) b[j] = sm.K[e * TS + x + 16 * j];
+        for (int j = 0; j < JN; ++j) {
+          const float b = tk[e * TS + x + 16 * j];
+          const uint64_t b2 = pair(b, b);
 #pragma unroll
-        for (int i = 0; i < RI; ++i)
-#pragma unroll
-          for (int j = 0; j < JN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+          for (int i = 0; i < RI / 2; ++i) acc[i][j] = fma2(a[i], b2, acc[i][j]);
+        }
       }
       const DecayStep f = decay_step(g, n);
 #pragma unroll
-      for (int i = 0; i < RI; ++i)
+      for (int i = 0; i < RI / 2; ++i)
 #pragma unroll
-        for (int j = 0; j < JN; ++j) s[i][j] = f(s[i][j], acc[i][j]);
+        for (int j = 0; j < JN; ++j) {
+          float d0, d1;
+          unpair(acc[i][j], d0, d1);
+          s[2 * i][j] = f(s[2 * i][j], d0);
+          s[2 * i + 1][j] = f(s[2 * i + 1][j], d1);
+        }
     }
     if (more) {
       if (OUT) publish_state();
-      __syncthreads();  // K and V are read
-      load(sm.K, k, qk_row, d_k, t0 + C);
-      load(sm.V, v, v_row, d_v, t0 + C);
+      __syncthreads();  // the keys and values are read
+      load(tk, v, v_row, d_v, t0 + C);
       copies_commit();
+      float* const old = tv;  // (free: the keys' next but one place)
+      tv = tk;
+      tk = spare;
+      spare = old;
     }
   }
   if (state.dst < 0) return;
