@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "gdn_internal.cuh"
 
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) 
     if (tid == 0) atomicExch(p.status, GDN_ERR_SHAPE);
     return;
   }
+  auto begun = cluster.barrier_arrive();  // (waited for before the first write to another CTA's memory)
   if (warp == 0) {
     int a = len;
     for (int j0 = 0; j0 < len; j0 += 32) {
@@ -194,6 +196,7 @@ __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) 
     sum = warp_sum(sum);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
+    if (pass == 0) cluster.barrier_wait(std::move(begun));  // every CTA of the cluster runs
     if (tid < ctas) {
       u64 cta = 0;
 #pragma unroll
