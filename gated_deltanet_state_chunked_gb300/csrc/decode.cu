@@ -15,7 +15,13 @@
 // reduced over the lanes that share it.  Longer windows go W tokens at a time, the state in registers.
 //
 // Layout: eight lanes share a row, lane l holding columns 4 (l & 7) + 32 j + [0, 4), so a warp's load
-// covers four rows in whole 128-byte lines.  Bound: HBM, 8 d_k d_v bytes per (request, v-head).
+// covers four rows in whole 128-byte lines.
+//
+// Bound: HBM, 8 d_k d_v bytes per (request, v-head), for single tokens.  Windows are bound by their
+// instructions (64 windows of 5 tokens, 32 heads of 128: 1290 a warp, 70 us with outputs against 20 us
+// of reading, 65 us committed against 38 us of traffic): two products of the whole state for each
+// token.  Measured and left: the products k_i.k_t from keys held in registers (they spill: 82 us),
+// keys and queries fetched before the state (77 us).
 #include <cuda_bf16.h>
 
 #include "gdn_internal.cuh"
@@ -61,8 +67,8 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // A window's products of keys and queries are worth sharing over a whole state: sixteen warps for
 // windows, eight for single tokens.  Either way 32 warps per SM at 64 registers a thread: what these
-// kernels need most is loads in flight (256 requests of 32 heads, one token: 171 us, against 176 us at
-// 24 warps and 216 us at 16).
+// kernels need most is loads in flight (256 requests of 32 heads, one token: 165 to 171 us, 95% of the
+// rate of a copy, against 176 us at 24 warps and 216 us at 16).
 __host__ __device__ constexpr int threads_of(int W) { return W == 1 ? 256 : 512; }
 
 // J: column groups of 32 (d_k at most 32 J); W: tokens unrolled at once; RG: groups of four rows per
@@ -97,11 +103,12 @@ __global__ void __launch_bounds__(threads_of(W), 1024 / threads_of(W)) decode_ke
       s[r][j] = (row < p.d_v && col < p.d_k) ? __ldcs(reinterpret_cast<const float4*>(Sb + (size_t)row * p.d_k + col))
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  // Two requests on one slot would race on its state: the first of them has it, the others are
-  // skipped and reported.  (Checked while the state's loads are in flight.)
+  // Two requests on one slot would race on its state: the first that updates it has it, the others
+  // are skipped and reported.  (Checked while the state's loads are in flight.)
   if (p.slots && !p.keep) {
     int dup = 0;
-    for (int j = tid; j < i; j += NT) dup |= p.slots[j] == slot;
+    for (int j = tid; j < i; j += NT)
+      dup |= p.slots[j] == slot && (!p.counts || (p.counts[j] > 0 && p.counts[j] <= p.window));
     if (__syncthreads_or(dup)) {
       if (tid == 0) atomicExch(p.status, GDN_ERR_SHAPE);
       return;
@@ -271,7 +278,7 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t stream) {
 template <typename Tin, int J, int W>
 cudaError_t launch_rows(const DecodeParams& p, cudaStream_t stream) {
   // Few states: 32 rows a CTA instead of 64, so that more SMs take part (one request of 32 heads, one
-  // token: 3.5 us against 4.4; four: 5.1 against 5.3; eight, 256 states: 9.7 against 8.8).
+  // token: 3.5 us against 4.4; four: 5.1 against 5.3; eight, 256 states: 9.7 against 8.8).  152: the SMs.
   const bool few = (long long)p.n * p.h_v < 152;
   if (p.family == kDelta) return few ? launch<Tin, J, W, 1, true>(p, stream) : launch<Tin, J, W, 2, true>(p, stream);
   return few ? launch<Tin, J, W, 1, false>(p, stream) : launch<Tin, J, W, 2, false>(p, stream);

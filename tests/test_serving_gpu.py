@@ -402,6 +402,21 @@ def test_decode_bad_slots_and_counts_are_reported():
                       before=torch.full((n * w, 2, 64), 7.0))
 
 
+def test_decode_same_slot_behind_an_empty_window():
+    """The first request that updates a slot has it, not one whose window counts no token."""
+    n, w = 4, 2
+    x = _decode_inputs(n, w, 1, 2, 64, 64, F32, 24, "delta", 4)
+    d = _cuda(x)
+    d["slots"] = torch.tensor([2, 2, 1, 2], dtype=torch.int32, device="cuda")
+    O = torch.full((n * w, 2, 64), 7.0, device="cuda")
+    api.gdn_decode(**d, counts=torch.tensor([0, 2, 1, 2], dtype=torch.int32, device="cuda"), O_out=O)
+    with pytest.raises(_lib.GdnError) as ei:
+        api.gdn_get_status()
+    assert ei.value.code == _lib.GDN_ERR_SHAPE
+    y = dict(x, slots=torch.tensor([-1, 2, 1, -1], dtype=torch.int32))
+    _check_decode(y, w, O, d["S_pool"], counts=[0, 2, 1, 0], before=torch.full((n * w, 2, 64), 7.0))
+
+
 def test_decode_same_slot_with_states_kept():
     """Requests may share a state that nobody writes (several drafted branches of one request)."""
     n, w = 3, 4
