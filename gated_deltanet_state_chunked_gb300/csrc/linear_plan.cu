@@ -230,8 +230,6 @@ cudaError_t launch_linear(const LinearParams& lp, int bf16, void* workspace, cud
   const Workspace w = workspace_of(lp, sms, tc);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const bool cut = w.cuts > 0, plan = lp.n_seqs > 1;
-  if ((long long)w.units * lp.h_v > INT_MAX || (long long)w.cut_units * lp.h_v > INT_MAX)
-    return cudaErrorInvalidConfiguration;
   LinearWork p{};
   p.q = lp.q; p.k = lp.k; p.v = lp.v; p.log_decay = lp.log_decay; p.cu = lp.cu; p.S0 = lp.S0;
   p.local = reinterpret_cast<float*>(ws + w.local); p.O = lp.O; p.S_out = lp.S_out; p.status = lp.status;

@@ -213,6 +213,10 @@ int gdn_compose(const gdn_dims* dims, int32_t K, const float* const* T, const fl
  *               every sequence's range are not written
  *   S_out       fp32 [n_seqs][h_v][d_v][d_k]; may alias S0
  * The state is carried in fp32 and at fp32 accuracy whatever the inputs' type.
+ * Scratch, from the library's pool and returned to it in stream order: a plan of the call when it has
+ * several sequences, and the states between the segments of prompts that are cut to fill the GPU (at
+ * most two states of d_v d_k floats per SM; nothing for a single short prompt).  The call can be
+ * captured into a graph and replayed with new contents.
  */
 int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
                     const int32_t* cu_seqlens, const float* S0, void* O_out, float* S_out, void* stream);
@@ -271,8 +275,8 @@ typedef struct {
  * Request by request: draft j is accepted while u_j * q_j(x_j) < p_j(x_j), in exact arithmetic.  Behind
  * the a accepted ones a token is sampled from the distribution max(p_a - q_a, 0) when draft a was
  * rejected (p_a itself where that is zero throughout), from p_a when every draft was accepted: the
- * lowest index whose inclusive sum of weights exceeds floor(u * sum), the weights whole multiples of
- * 2^-44 (each probability clamped to [0, 1] and rounded down; NaN counts as 0), so that the order of
+ * lowest index whose inclusive sum of weights exceeds floor(u * sum) (one product in fp64; a u outside
+ * [0, 1) takes the first or the last weight), the weights whole multiples of 2^-44 (each probability clamped to [0, 1] and rounded down; NaN counts as 0), so that the order of
  * summation cannot change the token.
  *   counts_out  int32 [n_seqs]: a + 1, the emitted tokens -- and, in a window of the last token
  *               followed by the drafts, the tokens that gdn_decode is to commit
@@ -297,7 +301,7 @@ int gdn_get_status(void* stream);
 /* Thread-local message of the last failed call ("" if none). */
 const char* gdn_last_error(void);
 
-/* Bytes of scratch the library's pool needs for this problem (0 if none). */
+/* Bytes of scratch the library's pool needs for a gdn_replay of this problem (0 if none). */
 size_t gdn_workspace_bytes(const gdn_dims* dims);
 
 /*

@@ -82,6 +82,12 @@ def test_linear_misaligned(lib, kw):
     assert _linear(lib, _dims(), **kw) == _lib.GDN_ERR_ALIGN
 
 
+def test_linear_more_work_than_a_launch_takes(lib):
+    for kw in (dict(n_seqs=2**31 - 1), dict(n_seqs=2**31 - 1, total_tokens=2**31 - 1, h_k=1, h_v=1),
+               dict(n_seqs=1 << 16, h_k=1 << 15, h_v=1 << 15), dict(n_seqs=0, total_tokens=2**31 - 1, h_k=1, h_v=256)):
+        assert _linear(lib, _dims(**kw)) == _lib.GDN_ERR_UNSUPPORTED, kw
+
+
 def test_replay_takes_no_decode_flags(lib):
     for flag in (_lib.GDN_HEAD_DECAY, _lib.GDN_KEEP_STATE):
         d = _dims(flags=flag)
