@@ -7,11 +7,17 @@
 //   P_ts = lambda^(t-s) q_t.k_s   (s <= t)
 //   O_t  = scale (sum_s P_ts v_s + lambda^(t+1) S q_t)
 //   S   <- lambda^n S + sum_s lambda^(n-1-s) v_s k_s^T
-// One CTA owns a (segment, v-head) and walks its chunks.  The state stays in registers, up to 8 x 8 entries
-// a thread, and is copied to shared memory, transposed, as the
-// readout's operand.  Every product is a register tile fed from shared memory: 4 x 4 for P (blocks above
-// the diagonal skipped), 8 rows x 4 columns for O, 8 x 8 for S, so that a fused multiply-add costs at
-// most three quarters of a shared-memory wavefront and the fp32 pipes are the bound.
+// One CTA owns a (segment, v-head) and walks its chunks.  The state stays in registers, up to 8 x 8
+// entries a thread, and is copied to shared memory, transposed, as the readout's operand.  Every product
+// is a register tile fed from shared memory: 4 x 4 for P (blocks above the diagonal skipped), 8 rows x 4
+// columns for O, 8 x 8 for S.  Keys, values and the next chunk's keys rotate through three buffers: the
+// values are weighted in place, and only their load waits for the end of a chunk.
+//
+// Bound: fp32 arithmetic and the shared-memory reads that feed it.  A chunk of 128 x 128 heads is 2.7 M
+// multiply-adds, 21,300 clocks of an SM's pipes; it takes about 39,000.  24 ragged prompts of 16,411
+// tokens in all (8/16 heads, d_k 96, d_v 120): 465 us (the tiles read without asynchronous copies: 523;
+// four multiply-adds where two packed ones are now: 478; one row a thread and no tiles: 3,830).  TF32
+// products on the tensor cores were not taken: three of them for fp32 accuracy run at 1.36 times this rate.
 #include "linear_work.cuh"
 #include "tc_common.cuh"
 
@@ -64,10 +70,16 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = tid & 15, y = tid >> 4;
   const int h = blockIdx.x % p.h_v, u = blockIdx.x / p.h_v;
   tc::grid_dep_launch();
-  if (p.list) tc::grid_dep_wait();  // the plan
+  // The plan; and no launch is over before the one ahead of it.  (Of a single sequence the segments with
+  // outputs load their inputs first and wait below.)
+  const bool later = OUT && !p.list;
+  if (!later) tc::grid_dep_wait();
   const Segment seg = p.list ? p.list[u] : only_segment(p, u);
   if (!p.list && blockIdx.x == 0 && tid == 0 && seg.seq < 0) atomicExch(p.status, GDN_ERR_SHAPE);
-  if (seg.seq < 0 || (p.local_only && seg.seg + 1 == seg.n_seg)) return;
+  if (seg.seq < 0 || (p.local_only && seg.seg + 1 == seg.n_seg)) {
+    tc::grid_dep_wait();
+    return;
+  }
   const ItemState state = item_state(p, seg, h, OUT);
   const int d_k = p.d_k, d_v = p.d_v, hk = h / (p.h_v / p.h_k);
   const float g = p.log_decay[h];
@@ -94,7 +106,7 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
   }
   copies_commit();
   for (int n = tid; n <= C; n += NT) sm.pw[n] = n ? expf((float)n * g) : 1.f;
-  if (OUT && seg.n_seg > 1) tc::grid_dep_wait();  // the entering states
+  if (later) tc::grid_dep_wait();  // the entering states
   float s[RI][JN];  // rows RI y + i, columns x + 16 j
 #pragma unroll
   for (int i = 0; i < RI; ++i)

@@ -22,9 +22,9 @@
 // The weighted values.  A state at fp32 accuracy needs the weight's 24 bits.  With the weight as three
 // bf16 terms w = a + b + c (8 bits each) the product with a bf16 value v splits without error:
 //   v a = h + r,  h = bf16(v a), r = v a - h;   v b = m + r',  m = bf16(v b);   l = bf16(v c + r')
-// so w v = h + r + m + l up to 2^-25, in five packed bf16 instructions for two values.  (Splitting the
-// fp32 product into three terms costs three times the instructions, which is what bound the kernel:
-// 785 us against 843 us for 64 prompts of 1556 tokens, 16/32 heads, before the other warps kept up.)
+// so w v = h + r + m + l up to 2^-25, in five packed bf16 instructions for two values.  (The fp32
+// product split into three terms needs a quarter fewer MMAs and three times the instructions: 32,768
+// tokens, 32 heads, state only, 135 us against 118; three terms by exact bf16 sums: 178.)
 //
 // Warpgroups (four warps; registers moved between them by setmaxnreg):
 //   0, 1  scores to P, outputs: a thread owns a row t, group 0 the column blocks 0 and 2 of the scores
@@ -37,6 +37,15 @@
 //
 // One CTA per SM stays and takes item after item (clusterlaunchcontrol): the loads, products and tables
 // of the next item start while the last chunks of the one before are finished.
+//
+// Bound: no single unit.  Per chunk with outputs (about 6,400 clocks) the shared-memory port is busy
+// for 4,000 (56 MMAs' operands, the copies, the staging), the tensor pipe for 56 MMAs, and each group's
+// loop is about as long as the chunk; at 64 prompts of 1556 tokens, 16/32 heads, the board's power limit
+// also holds the clock near 1.8 of 2.07 GHz.  Measured there: 605 us, 4.0 TB/s of 2.45 GB (665 us and
+// 4.1 TB/s with entering states; up to 717 us on boards that are held lower); one prompt of 3,277 tokens
+// 54 us, of 32,768 state only 115 us.  Measured and left at that first shape: QS issued by the KV warp
+// (640 to 690 us) or by the work's warp (683), PV before QS (787), outputs stored from registers (700),
+// outputs staged in Q's tile (647), other register shares (609 to 689).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
