@@ -10,9 +10,12 @@
 // split over threads, and with at most 2^19 entries a sum stays below 2^63.
 //
 // A cluster of CTAs shares a request: each warp sums a range of the row of its own, the CTAs tell each
-// other their totals through distributed shared memory, and the one warp whose range holds the sampled
-// place walks it again.  Bound: reading one row of p and, after a rejection, one of q, from HBM; for
-// few requests the chain of dependent reads (drafts, their probabilities, the row).
+// other their totals through distributed shared memory, the warps of the one CTA whose part of the row
+// holds the sampled place share the range that holds it, and one of them walks what is left of it.
+//
+// Bound: reading one row of p and, after a rejection, one of q, from HBM (128 requests over 131,072
+// entries: 31 us, 18 us of reading), with the chain of dependent reads around it (drafts, their
+// probabilities, the row, the walk: 6 us of one request over 32,000 entries).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -87,7 +90,7 @@ template <typename Tp, int NT, int MINB, int UNROLL>
 __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) {
   constexpr int NWARP = NT / 32;
   __shared__ int s_accept;
-  __shared__ u64 s_warp[NWARP];
+  __shared__ u64 s_warp[NWARP], s_sub[NWARP];
   __shared__ u64 s_cta[2][kMaxCluster];  // every CTA's total, of the weights, then (they are zero) of p alone
   const cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -146,9 +149,7 @@ __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) 
                        (4 * sizeof(Tp)) == 0;
   // Ranges of whole groups of 128 entries (four a lane), warp by warp, CTA by CTA.
   const int per = ((p.vocab + ctas * NWARP - 1) / (ctas * NWARP) + 127) / 128 * 128;
-  const int lo = min((rank * NWARP + warp) * per, p.vocab), hi = min(lo + per, p.vocab);
-
-  const bool drop = without >= lo && without < hi;  // the rejected token is in this warp's range
+  int lo = min((rank * NWARP + warp) * per, p.vocab), hi = min(lo + per, p.vocab);
   // Halves of the weights of entries [v, v + 4) of the range, one after another.
   auto weights = [&](bool minus, int v, int (&wh)[4], int (&wl)[4]) {
     const bool whole = vec && v + 4 <= hi;
@@ -181,47 +182,29 @@ __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) 
     for (int v = whole + lane; v < hi; v += 32) add_weight<Q>(prob(prow + v), Q ? prob(qrow + v) : 0.f, sh, sl);
   };
   bool minus = rejected;  // false: the weights are p's
-  u64 total = 0;
+  bool found = false;     // [lo, hi) is this warp's share of the range that holds the sampled place
+  u64 place = 0;          // from the sum before that range
+  const bool one_group = per == 128;
   for (int pass = 0;; ++pass) {
     int sh = 0, sl = 0;
-    if (minus && qrow) sums(std::true_type{}, sh, sl);
+    if (found && one_group) {}  // (what one step walks is not summed again)
+    else if (minus && qrow) sums(std::true_type{}, sh, sl);
     else sums(std::false_type{}, sh, sl);
-    if (minus && drop && lane == 0) {
+    if (minus && without >= lo && without < hi && lane == 0) {
       int wh = 0, wl = 0;
       add_weight<false>(prob(prow + without), 0.f, wh, wl);
       sh -= wh;
       sl -= wl;
     }
-    u64 sum = joined(sh, sl);
-    sum = warp_sum(sum);
-    if (lane == 0) s_warp[warp] = sum;
-    __syncthreads();
-    if (pass == 0) cluster.barrier_wait(std::move(begun));  // every CTA of the cluster runs
-    if (tid < ctas) {
-      u64 cta = 0;
-#pragma unroll
-      for (int w = 0; w < NWARP; ++w) cta += s_warp[w];
-      cluster.map_shared_rank(&s_cta[pass][0], tid)[rank] = cta;
-    }
-    cluster.sync();
-    total = 0;
-    for (int r = 0; r < ctas; ++r) total += s_cta[pass][r];
-    if (total > 0 || !minus) {
-      int32_t* out = p.tokens + trow;
-      if (rank == 0) {
-        for (int j = tid; j <= p.n_draft; j += NT)
-          if (j != a || total == 0) out[j] = j < a ? p.drafted[drow + j] : -1;
-        if (tid == 0) p.counts[i] = a + 1;
-      }
-      if (total == 0) return;
-      const double r = floor((double)u_last * (double)total);
-      // (r below 0 or NaN: the first place; r past the sum: the last)
-      u64 place = r > 0.0 ? (r < 9.2e18 ? (u64)r : total - 1) : 0;
-      place = place < total ? place : total - 1;
+    const u64 sum = warp_sum(joined(sh, sl));
+    if (found) {
       u64 before = 0;
-      for (int k = 0; k < rank; ++k) before += s_cta[pass][k];
-      for (int w = 0; w < warp; ++w) before += s_warp[w];
-      if (place < before || place - before >= s_warp[warp]) return;
+      if (!one_group) {
+        if (lane == 0) s_sub[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) before += s_sub[w];
+        if (place < before || place - before >= sum) return;
+      }
       for (int v0 = lo; v0 < hi; v0 += 128) {
         int wh[4], wl[4];
         u64 w[4], incl = 0;
@@ -241,7 +224,7 @@ __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) 
         if (over) {
           if (lane == __ffs(over) - 1) {
             const u64 s0 = before + incl - own + w[0], s1 = s0 + w[1], s2 = s1 + w[2];
-            out[a] = v0 + 4 * lane + (s0 > place ? 0 : s1 > place ? 1 : s2 > place ? 2 : 3);
+            p.tokens[trow + a] = v0 + 4 * lane + (s0 > place ? 0 : s1 > place ? 1 : s2 > place ? 2 : 3);
           }
           return;
         }
@@ -249,7 +232,50 @@ __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) 
       }
       return;
     }
-    minus = false;  // nothing is left of p: it is sampled itself
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+    if (pass == 0) cluster.barrier_wait(std::move(begun));  // every CTA of the cluster runs
+    if (tid < ctas) {
+      u64 cta = 0;
+#pragma unroll
+      for (int w = 0; w < NWARP; ++w) cta += s_warp[w];
+      cluster.map_shared_rank(&s_cta[pass][0], tid)[rank] = cta;
+    }
+    cluster.sync();
+    u64 total = 0, before = 0;  // before: this CTA's part of the row
+    for (int r = 0; r < ctas; ++r) {
+      if (r == rank) before = total;
+      total += s_cta[pass][r];
+    }
+    if (total == 0 && minus) {
+      minus = false;  // nothing is left of p: it is sampled itself
+      continue;
+    }
+    if (rank == 0) {
+      int32_t* out = p.tokens + trow;
+      for (int j = tid; j <= p.n_draft; j += NT)
+        if (j != a || total == 0) out[j] = j < a ? p.drafted[drow + j] : -1;
+      if (tid == 0) p.counts[i] = a + 1;
+    }
+    if (total == 0) return;
+    const double r = floor((double)u_last * (double)total);
+    // (r below 0 or NaN: the first place; r past the sum: the last)
+    place = r > 0.0 ? (r < 9.2e18 ? (u64)r : total - 1) : 0;
+    place = place < total ? place : total - 1;
+    if (place < before || place - before >= s_cta[pass][rank]) return;
+    place -= before;
+    int w = 0;
+    while (place >= s_warp[w]) place -= s_warp[w++];
+    found = true;
+    if (one_group) {
+      if (w != warp) return;
+      continue;
+    }
+    // The warps share that range, in whole groups of 128 entries.
+    const int from = (rank * NWARP + w) * per, to = min(from + per, p.vocab);
+    const int share = (per / 128 + NWARP - 1) / NWARP * 128;
+    lo = min(from + warp * share, to);
+    hi = min(lo + share, to);
   }
 }
 
@@ -269,8 +295,9 @@ cudaError_t launch(const VerifyParams& p, int ctas, cudaStream_t stream) {
 
 // CTAs per request: up to a portable cluster, while each gets 4096 entries.  Few requests take CTAs of
 // 512 threads, at most two an SM: a cluster's CTAs are placed as densely as they fit, and smaller ones
-// leave most SMs idle (16 requests over 131,072 entries: 15 us against 24 us).  With more CTAs than that
-// places, small ones, eight an SM, start in one wave (128 requests: 39 us against 49 us).
+// leave most SMs idle (16 requests over 131,072 entries: 11 us; 15 us against 24 us before the warps
+// shared the last range).  With more CTAs than that places, small ones, eight an SM, start in one wave
+// (128 requests: 31 us; 39 us against 49 us).
 template <typename Tp>
 cudaError_t launch_type(const VerifyParams& p, cudaStream_t stream) {
   constexpr int kTwoPerSm = 304;
