@@ -20,7 +20,7 @@
 // Bound: HBM, 8 d_k d_v bytes per (request, v-head), for single tokens (256 requests, 32 heads of 128:
 // 161 us, 97% of the rate of a copy).  Windows are bound by the latency of their steps (rows, products
 // of the window, sums, the triangular solve) with two states at a time on an SM, and their instructions:
-// 64 windows of 5 tokens, 32 heads of 128, take 45 us with outputs (20 us of reading) and 58 us
+// 64 windows of 5 tokens, 32 heads of 128, take 41 us with outputs (20 us of reading) and 56 us
 // committed (38 us of traffic).
 #include <cuda_bf16.h>
 
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kTokenNT, 4) decode_token_kernel(const DecodeP
   const int my_row = row0 + (second ? 4 : 0);
   const float v = my_row < p.d_v ? load1(static_cast<const Tin*>(p.v) + ((size_t)i * p.h_v + h) * p.d_v + my_row) : 0.f;
   if (warp == 0) {
-    const size_t at = ((size_t)i * p.h_k + h / (p.h_v / p.h_k)) * p.d_k + 4 * lane;
+    const size_t at = ((size_t)i * p.h_k + h / p.v_per_k) * p.d_k + 4 * lane;
     float4 k = make_float4(0.f, 0.f, 0.f, 0.f), q = k;
     if (4 * lane < p.d_k) {
       k = load4(static_cast<const Tin*>(p.k) + at);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(NT, blocks_of(RG, NT)) decode_window_kernel(co
   const int i = blockIdx.x, h = blockIdx.y;
   int slot, cnt;
   if (!request(p, i, slot, cnt)) return;
-  const int hk = h / (p.h_v / p.h_k);
+  const int hk = h / p.v_per_k;
   const int col0 = 4 * (lane & 7);
   const int row0 = blockIdx.z * (NW * 4 * RG) + warp * (4 * RG) + (lane >> 3);
   float* Sb = p.S + ((size_t)slot * p.h_v + h) * p.d_v * p.d_k;
@@ -250,9 +250,13 @@ __global__ void __launch_bounds__(NT, blocks_of(RG, NT)) decode_window_kernel(co
         }
       }
     }
+    const Tin* at = vp + (tok0 * p.h_v + h) * p.d_v + my_row;
+    const size_t step = (size_t)p.h_v * p.d_v;
 #pragma unroll
-    for (int t = 0; t < W; ++t)
-      v[t] = t < m && my_row < p.d_v ? load1(vp + ((tok0 + t) * p.h_v + h) * p.d_v + my_row) : 0.f;
+    for (int t = 0; t < W; ++t) {
+      v[t] = t < m && my_row < p.d_v ? load1(at) : 0.f;
+      at += step;
+    }
   };
   fetch(0);
   ulonglong2 s[RG][J];  // four columns, two by two
@@ -369,14 +373,20 @@ __global__ void __launch_bounds__(NT, blocks_of(RG, NT)) decode_window_kernel(co
         for (int e = 0; e < t; ++e) x = fmaf(-kk[t * (t + 1) / 2 + e], d[e], x);
       }
       d[t] = t < m ? beta[t] * x : 0.f;
-      if (want_o) {
-        float o = c * bm[t];
+      if (want_o) bm[t] *= c;
+    }
+    if (want_o) {
+      Tin* at = op + (tok0 * p.h_v + h) * p.d_v + my_row;
+      const size_t step = (size_t)p.h_v * p.d_v;
+#pragma unroll
+      for (int t = 0; t < W; ++t) {
+        float o = bm[t];
 #pragma unroll
         for (int e = 0; e <= t; ++e) o = fmaf(kq[t * (t + 1) / 2 + e], d[e], o);
         // (of the lanes that hold the row's sums, another one writes each token)
         constexpr int kSame = RG == 4 ? 1 : 7;
-        if (t < m && (lane & kSame) == (t & kSame) && my_row < p.d_v)
-          store1(op + ((tok0 + t) * p.h_v + h) * p.d_v + my_row, o);
+        if (t < m && (lane & kSame) == (t & kSame) && my_row < p.d_v) store1(at, o);
+        at += step;
       }
     }
     if (p.keep && t0 + W >= cnt) return;
@@ -432,13 +442,23 @@ void launch_token(const DecodeParams& p, bool few, cudaStream_t stream) {
   else decode_token_kernel<Tin, J, 2, DELTA><<<grid_of(p, kTokenNT / 4), kTokenNT, 0, stream>>>(p);
 }
 
-// (Heads of up to 64 rows: CTAs of that many; with 128 rows half of the warps would idle, 64 windows of 5
-// tokens and 64 x 64 heads: 19 us against 37.)
+// CTAs of 64 rows (four warps) for heads of up to 64 rows, where half of eight warps would idle (64
+// windows of 5 tokens, 64 x 64 heads: 19 us against 37), and for windows of up to 4 tokens, where four
+// CTAs an SM overlap better (of 2: 46 us against 50; of 4: 52 against 56); 128 rows for longer ones,
+// whose products would be computed twice (of 5: 42 us against 52).
 template <typename Tin, int J, int W, bool DELTA>
 void launch_window(const DecodeParams& p, bool few, cudaStream_t stream) {
-  if (few) decode_window_kernel<Tin, J, W, 1, 512, DELTA><<<grid_of(p, 64), 512, 0, stream>>>(p);
-  else if (p.d_v <= 64) decode_window_kernel<Tin, J, W, 4, 128, DELTA><<<grid_of(p, 64), 128, 0, stream>>>(p);
-  else decode_window_kernel<Tin, J, W, 4, 256, DELTA><<<grid_of(p, 128), 256, 0, stream>>>(p);
+  if (few) {
+    decode_window_kernel<Tin, J, W, 1, 512, DELTA><<<grid_of(p, 64), 512, 0, stream>>>(p);
+    return;
+  }
+  if constexpr (W > 4) {
+    if (p.d_v > 64) {
+      decode_window_kernel<Tin, J, W, 4, 256, DELTA><<<grid_of(p, 128), 256, 0, stream>>>(p);
+      return;
+    }
+  }
+  decode_window_kernel<Tin, J, W, 4, 128, DELTA><<<grid_of(p, 64), 128, 0, stream>>>(p);
 }
 
 template <typename Tin, int J, bool DELTA>

@@ -365,6 +365,7 @@ int gdn_decode(const gdn_dims* dims, int32_t n_slots, const void* q, const void*
   p.O = state_only ? nullptr : O_out;
   p.n = dims->n_seqs; p.window = dims->total_tokens / dims->n_seqs; p.n_slots = n_slots;
   p.h_k = dims->h_k; p.h_v = dims->h_v; p.d_k = dims->d_k; p.d_v = dims->d_v;
+  p.v_per_k = p.h_v / p.h_k;
   p.family = head ? kHeadDecay : (fl & GDN_SCALAR_DECAY) ? kScalarDecay : kDelta;
   p.l2norm = (fl & GDN_QK_L2NORM) ? 1 : 0; p.state_only = state_only ? 1 : 0; p.keep = keep ? 1 : 0;
   p.scale = dims->scale;

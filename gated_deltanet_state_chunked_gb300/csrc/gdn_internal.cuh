@@ -156,6 +156,7 @@ struct DecodeParams {
   void* O;
   int* status;
   int n, window, n_slots, h_k, h_v, d_k, d_v;
+  int v_per_k;  // h_v / h_k
   int family, l2norm, state_only, keep;
   float scale;
 };
