@@ -736,6 +736,25 @@ def test_decode_windows_longer_than_unrolled(n, w):
     _check_decode(x, w, O, d["S_pool"], counts=counts, before=torch.zeros(n * w, 2, 64, dtype=BF16))
 
 
+@pytest.mark.parametrize("w", range(2, 9))
+@pytest.mark.parametrize("n,h_k,h_v,d_k,d_v", [(80, 1, 2, 128, 128), (80, 2, 2, 72, 120), (80, 1, 2, 64, 40),
+                                               (3, 1, 2, 128, 128), (3, 1, 2, 40, 24)])
+def test_decode_every_window_length(n, h_k, h_v, d_k, d_v, w):
+    """Each unrolled length on few states and on many, on heads above and below 64 rows; windows of
+    which none, some or all tokens count, the rows behind them NaN."""
+    dt = BF16 if w % 2 else F32
+    x = _decode_inputs(n, w, h_k, h_v, d_k, d_v, dt, 700 + w, "delta", n + 2)
+    counts = [(3 * i + 1) % (w + 1) for i in range(n)]
+    d = _cuda(x)
+    for i in range(n):
+        for a in ("q", "k", "v", "g", "beta"):
+            d[a][i * w + counts[i]:(i + 1) * w] = float("nan")
+    O = torch.full((n * w, h_v, d_v), 7.0, dtype=dt, device="cuda")
+    api.gdn_decode(**d, counts=torch.tensor(counts, dtype=torch.int32, device="cuda"), O_out=O)
+    api.gdn_get_status()
+    _check_decode(x, w, O, d["S_pool"], counts=counts, before=torch.full((n * w, h_v, d_v), 7.0, dtype=dt))
+
+
 def test_decode_extreme_gates():
     """Gates from none to a full wipe (alpha = 0), per token and per head."""
     for family in ("delta", "scalar", "head"):
