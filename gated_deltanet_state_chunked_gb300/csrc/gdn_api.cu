@@ -287,8 +287,8 @@ int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const vo
   int rc = check_token_dims(dims);
   if (rc) return rc;
   if (dims->h_v > kMaxGridY) return fail(GDN_ERR_UNSUPPORTED, "h_v=%d above %d", dims->h_v, kMaxGridY);
-  // (a launch has a block for each segment, of 128 tokens or more unless it is a sequence's last, and v-head)
-  if (((long long)dims->n_seqs + dims->total_tokens / 128) * dims->h_v > INT32_MAX)
+  // (a launch has a block for each segment, of 64 tokens or more unless it is a sequence's last, and v-head)
+  if (((long long)dims->n_seqs + dims->total_tokens / 64) * dims->h_v > INT32_MAX)
     return fail(GDN_ERR_UNSUPPORTED, "n_seqs=%d, total_tokens=%d, h_v=%d: too many pieces of work", dims->n_seqs,
                 dims->total_tokens, dims->h_v);
   const bool state_only = dims->flags & GDN_STATE_ONLY;

@@ -150,12 +150,14 @@ __global__ void __launch_bounds__(kCarryNT) linear_carry_kernel(const LinearWork
   if (FINAL) *reinterpret_cast<float4*>(p.S_out + at) = E;
 }
 
-constexpr int kChunkTokens = 128;  // segments are whole chunks of either kernel
-// Cutting costs a launch for the segments' own states and one for their entering states, about 10 us,
-// and saves a chunk's time for each chunk that runs beside others: 3 us for 128 tokens on the tensor
-// cores (1024 tokens, 32 heads: 29 us cut in four, 35 us whole; 256 tokens: 23 and 12 us), 10 us for 64
-// tokens on the CUDA cores (8192 tokens, 2 heads: 76 us at the least segments, 246 us at 512 tokens).
-constexpr int kMinSegmentTc = 256, kMinTokensTc = 1024, kMinSegmentSimt = 128;
+// Cutting costs a launch for the segments' own states and one for their entering states, about 10 us on
+// the tensor cores and 5 us on the CUDA cores, and saves a chunk's time for each chunk that runs beside
+// others: 3 us for 128 tokens on the tensor cores (1024 tokens, 32 heads: 29 us cut in four, 35 us whole;
+// 256 tokens: 23 and 12 us), 9 to 20 us for 64 tokens on the CUDA cores, where a segment of one chunk
+// pays (2 heads of 128, 128 tokens: 34 us cut in two, 44 us whole; 1024 tokens: 36 us, 63 us at segments
+// of two chunks, 324 us whole).
+constexpr int kChunkTc = 128, kChunkSimt = 64;  // segments are whole chunks
+constexpr int kMinSegmentTc = 256, kMinTokensTc = 1024;
 
 // SMs of the current device, looked up once.
 cudaError_t device_sms(int* sms) {
@@ -174,10 +176,11 @@ cudaError_t device_sms(int* sms) {
 
 // Tokens per segment: one sequence's segments times the v-heads fill the GPU once.
 int segment_tokens(int total_tokens, int h_v, int sms, bool tc) {
-  if (tc && total_tokens < kMinTokensTc) return INT_MAX;
+  if (total_tokens < (tc ? kMinTokensTc : 1)) return INT_MAX;
   const int parts = std::max(1, sms / h_v);
-  const int seg = ((total_tokens + parts - 1) / parts + kChunkTokens - 1) / kChunkTokens * kChunkTokens;
-  return seg >= total_tokens ? INT_MAX : std::max(seg, tc ? kMinSegmentTc : kMinSegmentSimt);
+  const int chunk = tc ? kChunkTc : kChunkSimt;
+  const long long seg = ((total_tokens - 1) / parts / chunk + 1LL) * chunk;
+  return seg >= total_tokens ? INT_MAX : tc ? std::max((int)seg, kMinSegmentTc) : (int)seg;
 }
 
 // What a call keeps in its workspace: the plan's lists (none for one sequence), the cut segments' states.
