@@ -19,7 +19,8 @@
 // tokens in all (8/16 heads, d_k 96, d_v 120): 465 us (the tiles read without asynchronous copies: 523;
 // four multiply-adds where two packed ones are now: 478; rows of P V paired so that every warp has as many
 // tokens, and packed scores: 469 to 471, though 4% less at 128 x 128; one row a thread and no tiles: 3,830).  TF32
-// products on the tensor cores were not taken: three of them for fp32 accuracy run at 1.36 times this rate.
+// products on the warp-level tensor cores were not taken: three of them for fp32 accuracy run at 1.36 times
+// this rate.
 #include "linear_work.cuh"
 #include "tc_common.cuh"
 
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
           for (int e = 0; e < 2; ++e) o[i][e] = fma2(pair(f, f), o[i][e], 0);
         }
 #pragma unroll 2
-        for (int e0 = 0; e0 < 8 * warp + 8; e0 += 4) {  // (no later token counts for these rows)
+        for (int e0 = 0; e0 < 8 * warp; e0 += 4) {
           ulonglong2 b[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const ulonglong2*>(&tv[(e0 + e) * TS + col0]);
@@ -204,6 +205,23 @@ __global__ void __launch_bounds__(NT, 1) linear_simt_kernel(const LinearWork p) 
             rank1(a.y, b[1], o[i]);
             rank1(a.z, b[2], o[i]);
             rank1(a.w, b[3], o[i]);
+          }
+        }
+        // The warp's own eight tokens: a later one is left out, not multiplied by a score of zero (its
+        // value may be infinite).
+#pragma unroll
+        for (int e0 = 0; e0 < 8; e0 += 4) {
+          ulonglong2 b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const ulonglong2*>(&tv[(8 * warp + e0 + e) * TS + col0]);
+#pragma unroll
+          for (int i = 0; i < RI; ++i) {
+            const int last = row0 + i - 8 * warp - e0;  // of these four tokens, the last that is not later
+            const float4 a = *reinterpret_cast<const float4*>(&sm.P[(row0 + i) * PS + 8 * warp + e0]);
+            if (0 <= last) rank1(a.x, b[0], o[i]);
+            if (1 <= last) rank1(a.y, b[1], o[i]);
+            if (2 <= last) rank1(a.z, b[2], o[i]);
+            if (3 <= last) rank1(a.w, b[3], o[i]);
           }
         }
 #pragma unroll
