@@ -38,6 +38,14 @@
 // One CTA per SM stays and takes item after item (clusterlaunchcontrol): the loads, products and tables
 // of the next item start while the last chunks of the one before are finished.
 //
+// Infinite and NaN values.  P V multiplies a later token's value by a score of zero, which gives NaN where
+// the recurrence has nothing.  Such a value leaves its row of the state NaN for good, so the state's warps
+// see it at an item's end; the outputs it must not reach, at most 127 of a column, are computed again by
+// the recurrence behind the block's last item (amend_outputs).  Calls without such values pay one test per
+// item (64 prompts of 1556 tokens: 623 to 625 us).  Taking the values out of V's tile ahead of P V was
+// slower: seen by the splitting warps 690, by PV's own warp 695, by the work's warp 678; items done a
+// second time with V cleaned, 663.
+//
 // Bound: no single unit.  Per chunk with outputs (about 6,400 clocks) the shared-memory port is busy
 // for 4,000 (56 MMAs' operands, the copies, the staging), the tensor pipe for 56 MMAs, and each group's
 // loop is about as long as the chunk; at 64 prompts of 1556 tokens, 16/32 heads, the board's power limit
@@ -76,9 +84,17 @@ struct Item {
   int t_begin, n_last, h;
   float g;
   int dst, to_local;  // where the state behind the item goes: index of a state in S_out or in `local`; -1: nowhere
-  int pad;
+  int block;
   const float* S_in;  // entering state, or null (zero)
 };
+
+// 32 rows of half a state that an item left all NaN, and the item (its block index).
+struct NanRows {
+  int block, warp;  // of the state's warps
+  uint32_t rows;
+};
+// An item has at most 8 entries, and three more may be under way when the last steal is decided.
+constexpr int kNanMost = 32, kNanSteal = kNanMost - 3 * 8;
 
 // Shared memory: with outputs two stages of [Q | K | V] and the bf16 state (K-major); state only three
 // stages of [K | V].  The state's tile (there: a spare one) also stages entering and final states.
@@ -94,7 +110,8 @@ struct Lay {
   static constexpr uint32_t BARS = ITEM + 2 * 64;
   static constexpr uint32_t STEAL = BARS + 8 * 48;
   static constexpr uint32_t SCRATCH = STEAL + 16;
-  static constexpr uint32_t TOTAL = SCRATCH + 4 * 16;
+  static constexpr uint32_t NANS = SCRATCH + 4 * 16;
+  static constexpr uint32_t TOTAL = NANS + (OUT ? kNanMost * sizeof(NanRows) : 0);
   static_assert(sizeof(Item) <= 64 && TOTAL <= 232448, "shared memory");
 };
 // TMEM columns.  With outputs: QK (then P), O, KV, two A buffers; state only: two KV, four A buffers
@@ -195,6 +212,8 @@ __device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+// Whether a bf16 value is infinite or NaN.
+__device__ __forceinline__ bool not_finite(uint16_t x) { return (x & 0x7f80u) == 0x7f80u; }
 // 32 lanes x 16 columns (thread i -> lane i).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -236,6 +255,66 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+// What this thread's bulk copies wrote is there.
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ Segment segment_of(const LinearWork& p, int block) {
+  return p.list ? p.list[block / p.h_v] : only_segment(p, block / p.h_v);
+}
+
+// Behind the last item of a block, one warp a row d of a state that is NaN throughout.  In P V an infinite
+// or NaN value v_s[d] makes column d NaN for its whole chunk: the zero score of an earlier token times it
+// is NaN too.  The outputs of these earlier tokens are computed again by the recurrence; those of the
+// chunks before are right, and from s on they are not finite by definition.
+__device__ __forceinline__ void amend_outputs(const LinearWork& p, const NanRows& nan, int row) {
+  if (nan.warp >= 4 || !(nan.rows >> row & 1)) return;  // (both halves of a row are NaN then)
+  const Segment s = segment_of(p, nan.block);
+  const int h = nan.block % p.h_v, d = 32 * nan.warp + row, lane = threadIdx.x & 31;
+  const size_t v_step = (size_t)p.h_v * p.d_v, k_step = (size_t)p.h_k * p.d_k;
+  const size_t v_at = (size_t)s.t_begin * v_step + (size_t)h * p.d_v + d;
+  const size_t k_at = (size_t)s.t_begin * k_step + (size_t)(h / (p.h_v / p.h_k)) * p.d_k + 4 * lane;
+  const uint16_t* v = static_cast<const uint16_t*>(p.v) + v_at;
+  int first = s.len;  // the first such token
+#pragma unroll 1
+  for (int t0 = 0; t0 < s.len && first == s.len; t0 += 32) {
+    const unsigned found = __ballot_sync(0xffffffffu, t0 + lane < s.len && not_finite(v[(t0 + lane) * v_step]));
+    if (found) first = t0 + __ffs(found) - 1;
+  }
+  const int begin = first / C * C;
+  if (first == s.len || first == begin) return;
+  auto four = [&](const void* x, int t) {
+    uint2 u = make_uint2(0u, 0u);
+    if (4 * lane < p.d_k) u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + k_at + t * k_step);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+  };
+  const ItemState state = item_state(p, s, h, true);
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (state.S_in && 4 * lane < p.d_k) S = *reinterpret_cast<const float4*>(state.S_in + (size_t)d * p.d_k + 4 * lane);
+  const DecayStep f = decay_step(p.log_decay[h], 1);
+#pragma unroll 1
+  for (int t = 0; t < first; ++t) {
+    const float x = __uint_as_float((uint32_t)v[t * v_step] << 16);
+    const float4 k = four(p.k, t);
+    S = make_float4(f(S.x, x * k.x), f(S.y, x * k.y), f(S.z, x * k.z), f(S.w, x * k.w));
+    if (t < begin) continue;
+    const float4 q = four(p.q, t);
+    float o = fmaf(S.x, q.x, fmaf(S.y, q.y, fmaf(S.z, q.z, S.w * q.w)));
+#pragma unroll
+    for (int i = 16; i; i >>= 1) o += __shfl_xor_sync(0xffffffffu, o, i);
+    if (lane == 0) static_cast<__nv_bfloat16*>(p.O)[v_at + t * v_step] = __float2bfloat16_rn(p.scale * o);
+  }
+}
+// The half row of the final state, all NaN, in the place of the entering one.
+__device__ __forceinline__ void nan_row(const LinearWork& p, const NanRows& nan, int row) {
+  if (!(nan.rows >> row & 1)) return;
+  const ItemState state = item_state(p, segment_of(p, nan.block), nan.block % p.h_v, true);
+  if (state.dst < 0) return;
+  float* S = (state.to_local ? p.local : p.S_out) + ((size_t)state.dst * p.d_v + 32 * (nan.warp & 3) + row) * p.d_k;
+  const int lane = threadIdx.x & 31;
+  for (int c = 64 * (nan.warp >> 2) + lane; c < min(p.d_k, 64 * (nan.warp >> 2) + 64); c += 32) S[c] = __int_as_float(0x7fffffff);
+}
+
 // OUT: outputs and the final state; otherwise the states of the items alone (to S_out when a sequence
 // is one segment, to `local`, from zero, when it is cut).
 template <bool OUT>
@@ -253,6 +332,8 @@ __global__ void __launch_bounds__(NT, 1)
   volatile int* dead = scratch;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scratch + 1);
   int* issued = scratch + 2;  // chunks whose loads were issued
+  int* n_nans = scratch + 3;
+  NanRows* nans = reinterpret_cast<NanRows*>(sm + L::NANS);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2, quad = warp & 3;
   const int dkp = p.d_k <= 64 ? 64 : 128, dvp = p.d_v <= 64 ? 64 : 128;  // columns that the products cover
@@ -280,6 +361,7 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_fence_init();
     *dead = 0;
     *issued = 0;
+    *n_nans = 0;
   }
   tc_fence_before();
   __syncthreads();
@@ -620,6 +702,20 @@ __global__ void __launch_bounds__(NT, 1)
         }
       }
       if (!ok) break;
+      if (OUT && __any_sync(0xffffffffu, mine && s[0] != s[0])) {
+        // Rows that are NaN throughout, as an infinite or NaN value leaves them, are looked at behind the
+        // last item (amend_outputs), from their entering state: S_out may be its place, and keeps it till then.
+        bool all = mine;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) all = all && (64 * hw + j >= p.d_k || s[j] != s[j]);
+        const unsigned rows = __ballot_sync(0xffffffffu, all && r < p.d_v);
+        if (lane == 0 && rows) nans[atomicAdd(n_nans, 1)] = NanRows{item_at(k)->block, warp - 16, rows};
+        if (const float* S_in = item_at(k)->S_in) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if ((rows >> lane & 1) && 64 * hw + j < p.d_k) s[j] = S_in[(size_t)r * p.d_k + 64 * hw + j];
+        }
+      }
       if (item_at(k)->dst >= 0 && mine) {
         const CUtensorMap* map = item_at(k)->to_local ? &map_local : &map_s;
 #pragma unroll
@@ -866,6 +962,7 @@ __global__ void __launch_bounds__(NT, 1)
             it->S_in = state.S_in;
             it->to_local = state.to_local;
             it->dst = state.dst;
+            it->block = block;
             if (it->S_in) bulk_prefetch_l2(it->S_in, (uint32_t)(p.d_v * p.d_k * 4));
           }
           arrive(kItem + (k & 1));
@@ -873,6 +970,8 @@ __global__ void __launch_bounds__(NT, 1)
         }
         // (CTAs that were launched early take nothing from those that start when the kernel ahead ends)
         if (p.early) grid_dep_wait();
+        // (with many rows to look at again, this block ends, and others are launched for what is left)
+        if (OUT && *static_cast<volatile int*>(n_nans) >= kNanSteal) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar[kSteal], 16);
           steal_block(sm + L::STEAL, &bar[kSteal]);
@@ -899,6 +998,14 @@ __global__ void __launch_bounds__(NT, 1)
       atomicExch(p.status, GDN_ERR_TIMEOUT);
     }
     __syncthreads();
+  } else if (OUT && *n_nans > 0) {
+    bulk_wait_all();  // what this thread's copies store is there
+    __syncthreads();
+    if (group == 4 || group == 5)
+      for (int i = warp - 16; i < 32 * *n_nans; i += 8) amend_outputs(p, nans[i >> 5], i & 31);
+    __syncthreads();
+    if (group == 4 || group == 5)
+      for (int i = warp - 16; i < 32 * *n_nans; i += 8) nan_row(p, nans[i >> 5], i & 31);
   }
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);

@@ -213,6 +213,10 @@ int gdn_compose(const gdn_dims* dims, int32_t K, const float* const* T, const fl
  *               every sequence's range are not written
  *   S_out       fp32 [n_seqs][h_v][d_v][d_k]; may alias S0
  * The state is carried in fp32 and at fp32 accuracy whatever the inputs' type.
+ * An infinite or NaN value makes its row of the state, and that row's outputs, infinite or NaN from its
+ * token on (a key its column of the state and every output, a query its own outputs), and no earlier
+ * output.  With bf16 inputs a decay may hold partial sums 2^60 times as large as the outputs: they are
+ * finite while |sum (q.k) v| stays below 2^67.
  * Scratch, from the library's pool and returned to it in stream order: a plan of the call when it has
  * several sequences, and the states between the segments of prompts that are cut to fill the GPU (at
  * most two states of d_v d_k floats per SM; nothing for a single short prompt).  The call can be

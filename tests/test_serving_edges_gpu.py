@@ -67,7 +67,7 @@ def _check_not_finite(x, in_place=False):
             _same_where_finite(S2[i, h], S_ref[i, h], TOL_F32, ("S alone", i, h))
 
 
-NOT_FINITE_TYPES = [F32]
+NOT_FINITE_TYPES = [F32, BF16]
 SHAPES = [(1, 2, 128, 128), (2, 2, 64, 64), (1, 3, 72, 104), (1, 1, 96, 40)]
 
 
