@@ -38,7 +38,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 __device__ int g_status;  // sticky per-device status (one copy per device that loads the library)
 
 constexpr int kMaxGridY = 65535;    // v-heads of one launch of the prompt and decode kernels
-constexpr int kMaxVocab = 1 << 19;  // sums of 2^-44 fixed-point probabilities stay below 2^63
+constexpr int kMaxVocab = 1 << 19;  // sums of 2^-44 fixed-point probabilities are at most 2^63
 
 int check_head_dims(const gdn_dims* d) {
   if (d->h_k <= 0 || d->h_v <= 0) return fail(GDN_ERR_ARG, "h_k and h_v must be positive");

@@ -7,7 +7,7 @@
 //   the lowest index whose inclusive sum of W exceeds floor(u_w sum W).
 // Probabilities enter the sums as whole multiples of 2^-44 (rounded down, clamped to [0, 1], NaN
 // as 0): whole-number sums are the same in any order, so the token never depends on how the row is
-// split over threads, and with at most 2^19 entries a sum stays below 2^63.
+// split over threads, and with at most 2^19 entries a sum is at most 2^63, in unsigned 64 bits.
 //
 // A cluster of CTAs shares a request: each warp sums a range of the row of its own, the CTAs tell each
 // other their totals through distributed shared memory, the warps of the one CTA whose part of the row
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(NT, MINB) verify_kernel(const VerifyParams p) 
     if (total == 0) return;
     const double r = floor((double)u_last * (double)total);
     // (r below 0 or NaN: the first place; r past the sum: the last)
-    place = r > 0.0 ? (r < 9.2e18 ? (u64)r : total - 1) : 0;
-    place = place < total ? place : total - 1;
+    place = r > 0.0 ? (r < (double)total ? (u64)r : total - 1) : 0;
+    place = place < total ? place : total - 1;  // ((double)total may be rounded up)
     if (place < before || place - before >= s_cta[pass][rank]) return;
     place -= before;
     int w = 0;

@@ -140,3 +140,21 @@ def test_prompt_values_that_are_no_numbers_in_many_sequences(dt):
             x["v"][at, 0, i % 64] = (INF, NAN, -INF)[i % 3]
     x["log_decay"][0] = -0.02
     _check_not_finite(x)
+
+
+# ------------------------------------------------------------------ verification
+
+
+@pytest.mark.parametrize("vocab", [1 << 19, (1 << 19) - 1, 1000])
+def test_verify_rows_of_ones(vocab):
+    """Rows that add up to vocab, at most 2^63 in units of 2^-44: entry floor(u vocab 2^44) >> 44 is drawn
+    (whole numbers; u vocab 2^44 is exact in fp64 for a power of two, else rounded once)."""
+    u = [0.0, 0.5, 0.9979, 0.9984, 0.999, 0.99999994, 1.0, 1.5]
+    uniforms = torch.tensor(u, dtype=F32).reshape(-1, 1)
+    target = torch.ones((1, 1, vocab), device="cuda").repeat(len(u), 1, 1)
+    counts, tokens = api.gdn_verify_draft(target, torch.empty((len(u), 0), dtype=torch.int32, device="cuda"),
+                                          uniforms.cuda())
+    api.gdn_get_status()
+    total = vocab << 44
+    want = [min(int(float(x) * float(total)), total - 1) >> 44 for x in uniforms.flatten()]
+    assert counts.tolist() == [1] * len(u) and tokens.flatten().tolist() == want
