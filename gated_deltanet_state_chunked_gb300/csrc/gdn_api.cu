@@ -294,7 +294,7 @@ int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const vo
   const bool state_only = dims->flags & GDN_STATE_ONLY;
   if (dims->n_seqs == 0) return GDN_OK;
   if (!cu_seqlens || !S_out || !log_decay) return fail(GDN_ERR_ARG, "cu_seqlens, log_decay and S_out are required");
-  if (!state_only && !O_out) return fail(GDN_ERR_ARG, "O_out is NULL without GDN_STATE_ONLY");
+  if (!state_only && !O_out && dims->total_tokens > 0) return fail(GDN_ERR_ARG, "O_out is NULL without GDN_STATE_ONLY");
   if (dims->total_tokens > 0 && ((!q && !state_only) || !k || !v))
     return fail(GDN_ERR_ARG, "q (unless GDN_STATE_ONLY), k and v are required when total_tokens > 0");
   const void* p16[] = {q, k, v, O_out, S0, S_out};

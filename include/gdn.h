@@ -209,8 +209,8 @@ int gdn_compose(const gdn_dims* dims, int32_t K, const float* const* T, const fl
  *   log_decay   fp32 device [h_v], <= 0 (0: no decay; -inf: each token's state is its own)
  *   cu_seqlens  int32 device [n_seqs + 1]; malformed ranges are skipped and reported as in gdn_replay
  *   S0          fp32 [n_seqs][h_v][d_v][d_k] or NULL (zero); a sequence of no tokens returns it
- *   O_out       [total_tokens][h_v][d_v] in `dims->dtype`, NULL iff GDN_STATE_ONLY; rows outside
- *               every sequence's range are not written
+ *   O_out       [total_tokens][h_v][d_v] in `dims->dtype`, NULL with GDN_STATE_ONLY (and where there
+ *               are no tokens); rows outside every sequence's range are not written
  *   S_out       fp32 [n_seqs][h_v][d_v][d_k]; may alias S0
  * The state is carried in fp32 and at fp32 accuracy whatever the inputs' type.
  * An infinite or NaN value makes its row of the state, and that row's outputs, infinite or NaN from its

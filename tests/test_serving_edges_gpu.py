@@ -142,6 +142,19 @@ def test_prompt_values_that_are_no_numbers_in_many_sequences(dt):
     _check_not_finite(x)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("state_only", [False, True])
+def test_prompt_of_no_tokens(dt, n, state_only):
+    """Empty prompts return their entering states, or zero."""
+    x = _cuda(_prompt([0] * n, 1, 2, 64, 72, dt, 3800))
+    O, S = api.gdn_linear_attn(**x, state_only=state_only)
+    _, S2 = api.gdn_linear_attn(**dict(x, S0=None), state_only=state_only)
+    api.gdn_get_status()
+    assert torch.equal(S, x["S0"]) and float(S2.abs().max()) == 0.0
+    assert O is None if state_only else O.shape == (0, 2, 72)
+
+
 # ------------------------------------------------------------------ verification
 
 
