@@ -1,7 +1,6 @@
 // C ABI of libgdn.so: argument checks, dispatch to the kernels, status word.
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdio>
 #include <cstring>
 #include <cstdarg>
@@ -135,15 +134,9 @@ unsigned long long take_wait_limit_ns() {
   return ns;
 }
 
-int* device_status_word() {
-  static std::atomic<void*> known[64];  // per device (the symbol's address on it)
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  const bool keep = dev >= 0 && dev < 64;
-  void* p = keep ? known[dev].load(std::memory_order_acquire) : nullptr;
-  if (p) return static_cast<int*>(p);
+int* device_status_word() {  // (looked up in each call: the address is the current context's)
+  void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
-  if (keep) known[dev].store(p, std::memory_order_release);
   return static_cast<int*>(p);
 }
 
