@@ -1038,28 +1038,20 @@ bool make_map_states(CUtensorMap* m, const void* base, size_t count, int d_v, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The kernels may have their shared memory, and are launched with the registers that the warpgroups'
-// shares add up to (with fewer, a warpgroup that asks for more would wait): checked once per device.
-cudaError_t prepare_device() {
-  constexpr int kDevices = 64;
-  static std::atomic<bool> ready[kDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
-  if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+// The kernels are launched with the registers that the warpgroups' shares add up to (with fewer, a
+// warpgroup that asks for more would wait): checked once.
+cudaError_t check_registers() {
+  static std::atomic<bool> checked{false};
+  if (checked.load(std::memory_order_acquire)) return cudaSuccess;
   const void* kernels[] = {reinterpret_cast<const void*>(linear_tc_kernel<true>),
                            reinterpret_cast<const void*>(linear_tc_kernel<false>)};
-  const int bytes[] = {(int)Lay<true>::TOTAL, (int)Lay<false>::TOTAL};
-  for (int i = 0; i < 2; ++i) {
+  for (const void* kernel : kernels) {
     cudaFuncAttributes have;
-    e = cudaFuncGetAttributes(&have, kernels[i]);
+    const cudaError_t e = cudaFuncGetAttributes(&have, kernel);
     if (e != cudaSuccess) return e;
     if (have.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-    e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]);
-    if (e != cudaSuccess) return e;
   }
-  ready[dev].store(true, std::memory_order_release);
+  checked.store(true, std::memory_order_release);
   return cudaSuccess;
 }
 
@@ -1073,6 +1065,10 @@ cudaError_t launch_items(const LinearWork& p, int units, cudaStream_t stream) {
       !make_map_states(&ms, p.S_out, (size_t)p.n_seqs * p.h_v, p.d_v, p.d_k) ||
       (p.cut_units > 0 && !make_map_states(&ml, p.local, (size_t)p.cut_units * p.h_v, p.d_v, p.d_k)))
     return cudaErrorInvalidValue;
+  // (in each call: the attribute belongs to the current context)
+  const cudaError_t e =
+      cudaFuncSetAttribute(linear_tc_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<OUT>::TOTAL);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units * p.h_v);
   cfg.blockDim = dim3(NT);
@@ -1089,7 +1085,7 @@ cudaError_t launch_items(const LinearWork& p, int units, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_linear_tc_items(const LinearWork& p, bool out, int units, cudaStream_t stream) {
-  const cudaError_t e = prepare_device();
+  const cudaError_t e = check_registers();
   if (e != cudaSuccess) return e;
   return out ? launch_items<true>(p, units, stream) : launch_items<false>(p, units, stream);
 }

@@ -47,7 +47,19 @@ def bad_draft_length():
     assert host(out, 16) == struct.pack("4i", 7, 7, 7, 7)
 
 
-CALLS = [bad_draft_length]
+def prompt_of_one_token():
+    # S = v k^T and o = (k.q) v, whole numbers in bf16
+    d = 64
+    dims = _lib.GdnDims(1, 1, 1, 1, d, d, _lib.GDN_BF16, 0, 1.0)
+    q, k, v = (device(struct.pack("H", bits) * d) for bits in (0x3F80, 0x3F00, 0x4000))  # 1, 1/2 and 2
+    O, S = device(bytes(2 * d)), device(bytes(4 * d * d))
+    ok(lib.gdn_linear_attn(ctypes.byref(dims), q, k, v, device(bytes(4)), device(struct.pack("2i", 0, 1)), None, O, S, None))
+    ok(lib.gdn_get_status(None))
+    assert host(S, 4 * d * d) == struct.pack("f", 1.0) * (d * d)
+    assert host(O, 2 * d) == struct.pack("H", 0x4280) * d  # 64
+
+
+CALLS = [bad_draft_length, prompt_of_one_token]
 
 
 def main():
