@@ -37,6 +37,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 __device__ int g_status;  // sticky per-device status (one copy per device that loads the library)
 
 constexpr int kMaxGridY = 65535;    // v-heads of one launch of the prompt and decode kernels
+constexpr int kMaxRows = INT32_MAX - 1023;  // tokens or drafts of a serving call: the kernels step past the last in 32 bits
 constexpr int kMaxVocab = 1 << 19;  // sums of 2^-44 fixed-point probabilities are at most 2^63
 
 int check_head_dims(const gdn_dims* d) {
@@ -280,6 +281,7 @@ int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const vo
   int rc = check_token_dims(dims);
   if (rc) return rc;
   if (dims->h_v > kMaxGridY) return fail(GDN_ERR_UNSUPPORTED, "h_v=%d above %d", dims->h_v, kMaxGridY);
+  if (dims->total_tokens > kMaxRows) return fail(GDN_ERR_UNSUPPORTED, "total_tokens=%d above %d", dims->total_tokens, kMaxRows);
   // (a launch has a block for each segment, of 64 tokens or more unless it is a sequence's last, and v-head)
   if (((long long)dims->n_seqs + dims->total_tokens / 64) * dims->h_v > INT32_MAX)
     return fail(GDN_ERR_UNSUPPORTED, "n_seqs=%d, total_tokens=%d, h_v=%d: too many pieces of work", dims->n_seqs,
@@ -337,6 +339,7 @@ int gdn_decode(const gdn_dims* dims, int32_t n_slots, const void* q, const void*
   if (state_only && keep) return fail(GDN_ERR_ARG, "GDN_STATE_ONLY with GDN_KEEP_STATE leaves nothing to do");
   if (head && (fl & GDN_SCALAR_DECAY)) return fail(GDN_ERR_ARG, "GDN_HEAD_DECAY and GDN_SCALAR_DECAY exclude each other");
   if (dims->h_v > kMaxGridY) return fail(GDN_ERR_UNSUPPORTED, "h_v=%d above %d", dims->h_v, kMaxGridY);
+  if (dims->total_tokens > kMaxRows) return fail(GDN_ERR_UNSUPPORTED, "total_tokens=%d above %d", dims->total_tokens, kMaxRows);
   if (n_slots < 0) return fail(GDN_ERR_ARG, "negative n_slots");
   if (dims->n_seqs == 0 || dims->total_tokens == 0) return GDN_OK;
   if (dims->total_tokens % dims->n_seqs)
@@ -377,6 +380,7 @@ int gdn_verify_draft(const gdn_verify_dims* dims, const void* target, const void
   if (dims->n_seqs < 0 || dims->n_draft < 0) return fail(GDN_ERR_ARG, "negative n_seqs or n_draft");
   if (dims->vocab <= 0) return fail(GDN_ERR_ARG, "vocab must be positive");
   if (dims->dtype != GDN_F32 && dims->dtype != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d", dims->dtype);
+  if (dims->n_draft > kMaxRows) return fail(GDN_ERR_UNSUPPORTED, "n_draft=%d above %d", dims->n_draft, kMaxRows);
   if (dims->vocab > kMaxVocab) return fail(GDN_ERR_UNSUPPORTED, "vocab=%d above %d", dims->vocab, kMaxVocab);
   if (dims->target_stride < dims->vocab || (draft && dims->draft_stride < dims->vocab))
     return fail(GDN_ERR_SHAPE, "a row stride is below vocab (%d)", dims->vocab);

@@ -204,7 +204,8 @@ int gdn_compose(const gdn_dims* dims, int32_t K, const float* const* T, const fl
  * for Position-Independent Caching in Hybrid LLMs" (composition passage) sets
  * beside the delta rule, with a transition that belongs to the head alone:
  *     S_t = lambda_h S_{t-1} + v_t k_t^T,   o_t = S_t (scale * q_t),   lambda_h = exp(log_decay[h]).
- *   dims        as gdn_replay's; the only flag taken is GDN_STATE_ONLY (q and k are used as given)
+ *   dims        as gdn_replay's; the only flag taken is GDN_STATE_ONLY (q and k are used as given);
+ *               at most 2^31 - 1024 tokens
  *   q, k, v     inputs in `dims->dtype`, layouts above (q may be NULL with GDN_STATE_ONLY)
  *   log_decay   fp32 device [h_v], <= 0 (0: no decay; -inf: each token's state is its own)
  *   cu_seqlens  int32 device [n_seqs + 1]; malformed ranges are skipped and reported as in gdn_replay
@@ -232,7 +233,7 @@ int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const vo
  * GDN_SCALAR_DECAY or GDN_HEAD_DECAY the scalar-transition families), readout with
  * the updated state as in gdn_replay.
  *   dims        n_seqs requests; total_tokens = n_seqs * window: request i's tokens are rows
- *               [i * window, (i + 1) * window) of q, k, v, g, beta and O
+ *               [i * window, (i + 1) * window) of q, k, v, g, beta and O; at most 2^31 - 1024 of them
  *   n_slots     states in the pool
  *   g, beta     fp32 [total_tokens][h_v]; with GDN_HEAD_DECAY g is the log decay [h_v] and beta NULL
  *   slots       int32 device [n_seqs]: each request's state in the pool; NULL: request i has state i.
@@ -256,7 +257,7 @@ int gdn_decode(const gdn_dims* dims, int32_t n_slots, const void* q, const void*
 
 typedef struct {
   int32_t n_seqs;        /* requests */
-  int32_t n_draft;       /* drafted tokens per request (the most, with draft_lens) */
+  int32_t n_draft;       /* drafted tokens per request (the most, with draft_lens), at most 2^31 - 1024 */
   int32_t vocab;         /* entries of a probability row, at most 524288 */
   int32_t dtype;         /* of target and draft: GDN_F32 or GDN_BF16 */
   int64_t target_stride; /* elements between consecutive rows of target, at least vocab */
