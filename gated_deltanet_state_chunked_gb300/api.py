@@ -193,6 +193,12 @@ def _want(name, t, device, dtype, shape):
     return t.data_ptr()
 
 
+def _fits(*sizes):
+    """The C structures hold 32 bits, and what is more would be cut off without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"a size of {max(sizes)} does not fit in 32 bits")
+
+
 def _cuda_index(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -237,6 +243,7 @@ def gdn_linear_attn(q, k, v, log_decay, cu_seqlens, S0=None, *, O_out=None, S_ou
         raise ValueError(f"unsupported dtype {dt}")
     if q is None and not state_only:
         raise ValueError("q may be None only with state_only")
+    _fits(n, T, h_k, h_v, d_k, d_v)
     dev = _cuda_index("k", k)
     qk, vo, state = (T, h_k, d_k), (T, h_v, d_v), (n, h_v, d_v, d_k)
     args = (_want("q", q, dev, dt, qk), _want("k", k, dev, dt, qk), _want("v", v, dev, dt, vo),
@@ -274,6 +281,7 @@ def gdn_decode(q, k, v, g, beta, S_pool, slots=None, *, counts=None, O_out=None,
         raise ValueError("q may be None only with state_only")
     if n == 0 and T:
         raise ValueError(f"{T} tokens of no requests")
+    _fits(n, n_slots, T, h_k, h_v, d_k, d_v)
     dev = _cuda_index("k", k)
     qk, vo, per = (T, h_k, d_k), (T, h_v, d_v), (T, h_v)
     args = (n_slots, _want("q", q, dev, dt, qk), _want("k", k, dev, dt, qk), _want("v", v, dev, dt, vo),
@@ -321,6 +329,7 @@ def gdn_verify_draft(target, drafted, uniforms, draft=None, draft_lens=None, *, 
     dt = target.dtype
     if dt not in _DTYPE:
         raise ValueError(f"unsupported dtype {dt}")
+    _fits(n, n_draft, vocab)
     dev = _cuda_index("target", target)
     target_stride = _prob_rows("target", target, (n, n_draft + 1, vocab))
     draft_stride, draft_ptr = 0, None

@@ -2,8 +2,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from gated_deltanet_state_chunked_gb300 import _lib
+from gated_deltanet_state_chunked_gb300 import _lib, api
 
 A = ctypes.c_void_p(1 << 20)  # aligned fake address, never dereferenced
 MOST = 2**31 - 1
@@ -27,3 +28,19 @@ def test_more_tokens_than_32_bits_step_over(lib, tokens, dtype):
 def test_more_drafts_than_32_bits_step_over(lib, n_draft):
     dims = _lib.GdnVerifyDims(2, n_draft, 1, _lib.GDN_BF16, 1, 1)
     assert lib.gdn_verify_draft(ctypes.byref(dims), A, None, A, None, A, A, A, None) == _lib.GDN_ERR_UNSUPPORTED
+
+
+def test_binding_refuses_what_32_bits_cut_off(lib):
+    """2^32 + 4 tokens are not four of them (tensors without storage)."""
+    far = 2**32 + 4
+
+    def empty(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    k, g = empty(far, 1, 8), empty(far, 1, dtype=torch.float32)
+    with pytest.raises(ValueError, match="32 bits"):
+        api.gdn_linear_attn(k, k, k, g[0], empty(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="32 bits"):
+        api.gdn_decode(k, k, k, g, g, empty(1, 1, 8, 8, dtype=torch.float32))
+    with pytest.raises(ValueError, match="32 bits"):
+        api.gdn_verify_draft(empty(1, 1, far), empty(1, 0, dtype=torch.int32), empty(1, 1, dtype=torch.float32))
