@@ -201,3 +201,68 @@ def test_prompt_thousands_of_sequences(dt, state_only, d_k, d_v):
         done[a:b] = True
     assert bool(((O - O_ref).abs() <= bound)[done].all())
     assert bool((O[~done] == 7.0).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("state_only", [False, True])
+@pytest.mark.parametrize("a,b", [(0, 3000), (37, 500), (5, 2400), (2990, 3000), (40, 40), (3000, 3000), (10, 5), (-1, 64),
+                                 (100, 3001)])
+def test_prompt_one_sequence_inside_its_tensor(dt, state_only, a, b):
+    """A call is cut by the tokens its tensors have; its only sequence may be shorter, empty or malformed."""
+    gen = _gen(1300)
+    T, d_k, d_v = 3000, 64, 72
+    q, k = (torch.nn.functional.normalize(torch.randn(T, 1, d_k, generator=gen), dim=-1).to(dt) for _ in range(2))
+    v, g, S0 = torch.randn(T, 1, d_v, generator=gen).to(dt), torch.tensor([-0.01]), torch.randn(1, 1, d_v, d_k, generator=gen)
+    S = torch.full((1, 1, d_v, d_k), 5.0, device="cuda")
+    O = None if state_only else torch.full((T, 1, d_v), 7.0, dtype=dt, device="cuda")
+    api.gdn_linear_attn(q.cuda(), k.cuda(), v.cuda(), g.cuda(), torch.tensor([a, b], dtype=torch.int32, device="cuda"),
+                        S0.cuda(), S_out=S, O_out=O, state_only=state_only)
+    good = 0 <= a <= b <= T
+    if not good:
+        with pytest.raises(_lib.GdnError) as ei:
+            api.gdn_get_status()
+        assert ei.value.code == _lib.GDN_ERR_SHAPE
+        a = b = 0
+    api.gdn_get_status()
+    O_ref, S_ref = _prompt_reference(q[:, 0], k[:, 0], v[:, 0], g, S0[:, 0], [(a, b)])
+    size, _ = _prompt_reference(q[:, 0].abs(), k[:, 0].abs(), v[:, 0].abs(), g, S0[:, 0].abs(), [(a, b)])
+    S = S.cpu().double()[:, 0]
+    assert float((S - S_ref).norm()) <= TOL_F32 * float(S_ref.norm()) if good else bool((S == 5.0).all())
+    if O is not None:
+        O, r = O.cpu().double()[:, 0], 2.0 ** -8 if dt == BF16 else 0.0
+        assert bool(((O - O_ref).abs() <= r * O_ref.abs() + (1.02 * r + TOL_F32) * size)[a:b].all())
+        assert bool((O[:a] == 7.0).all()) and bool((O[b:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("h_k,h_v", [(300, 300), (100, 200)])
+def test_more_heads_than_multiprocessors(dt, h_k, h_v):
+    """Sequences are not cut then; decode has as many states in one request."""
+    gen = _gen(1400 + h_v)
+    lens, d_k, d_v = [1100, 0, 70], 16, 24
+    T, n = sum(lens), len(lens)
+    q, k = (torch.nn.functional.normalize(torch.randn(T, h_k, d_k, generator=gen), dim=-1).to(dt) for _ in range(2))
+    v, g = torch.randn(T, h_v, d_v, generator=gen).to(dt), -torch.exp2(-8 * torch.rand(h_v, generator=gen))
+    S0 = torch.randn(n, h_v, d_v, d_k, generator=gen)
+    cu = torch.tensor([0, 1100, 1100, 1170])
+    O, S = api.gdn_linear_attn(q.cuda(), k.cuda(), v.cuda(), g.cuda(), cu.to(torch.int32).cuda(), S0.cuda())
+    api.gdn_get_status()
+    O, S = O.cpu().double(), S.cpu().double()
+    ranges = list(zip(cu.tolist(), cu.tolist()[1:]))
+    r = 2.0 ** -8 if dt == BF16 else 0.0
+    for h in (0, 1, h_v // 2, h_v - 1):
+        one = (q[:, h * h_k // h_v], k[:, h * h_k // h_v], v[:, h])
+        O_ref, S_ref = _prompt_reference(*one, g[h], S0[:, h], ranges)
+        size, _ = _prompt_reference(*(t.abs() for t in one), g[h], S0[:, h].abs(), ranges)
+        err = (S[:, h] - S_ref).flatten(1).norm(dim=-1) / S_ref.flatten(1).norm(dim=-1)
+        assert float(err.max()) <= TOL_F32
+        assert bool(((O[:, h] - O_ref).abs() <= r * O_ref.abs() + (1.02 * r + TOL_F32) * size).all())
+    x = _decode_inputs(2, 1, h_k, h_v, d_k, d_v, dt, "delta", 1500 + h_v)
+    O_ref, S_ref = _decode_reference(x, torch.tensor([1, 1]), "delta")
+    pool = x["pool"].cuda()
+    O = api.gdn_decode(*(x[a].flatten(0, 1).cuda() for a in ("q", "k", "v", "g", "beta")), pool, x["slots"].to(torch.int32).cuda())
+    api.gdn_get_status()
+    got = pool.cpu()[x["slots"]].double()
+    assert float(((got - S_ref).flatten(2).norm(dim=-1) / S_ref.flatten(2).norm(dim=-1)).max()) <= 2e-6
+    bound = 2e-6 * O_ref.norm(dim=(-2, -1), keepdim=True) + r * O_ref.abs()
+    assert bool(((O.cpu().double().view(2, 1, h_v, d_v) - O_ref).abs() <= bound).all())
