@@ -266,3 +266,26 @@ def test_more_heads_than_multiprocessors(dt, h_k, h_v):
     assert float(((got - S_ref).flatten(2).norm(dim=-1) / S_ref.flatten(2).norm(dim=-1)).max()) <= 2e-6
     bound = 2e-6 * O_ref.norm(dim=(-2, -1), keepdim=True) + r * O_ref.abs()
     assert bool(((O.cpu().double().view(2, 1, h_v, d_v) - O_ref).abs() <= bound).all())
+
+
+def test_more_exact_ways_to_a_bf16_prompt():
+    """What the header names for callers who need more than bf16 outputs give: widened inputs, and the replay
+    of the scalar family with one decay per head.  Both are the same recurrence; the replay at fp32 accuracy
+    rounds its outputs alone (2^-8 of each value)."""
+    gen = _gen(1600)
+    T, h_k, h_v, d = 700, 1, 2, 128
+    q, k = (torch.nn.functional.normalize(torch.randn(T, h_k, d, generator=gen), dim=-1).to(BF16).cuda() for _ in range(2))
+    v, g = torch.randn(T, h_v, d, generator=gen).to(BF16).cuda(), torch.tensor([-0.4, -0.004]).cuda()
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    O1, S1 = api.gdn_linear_attn(q.float(), k.float(), v.float(), g, cu)
+    O2, S2 = api.gdn_replay(q, k, v, g.expand(T, h_v).contiguous(), torch.ones(T, h_v, device="cuda"), cu, l2norm_qk=False,
+                            scalar_decay=True, precise=True)
+    api.gdn_get_status()
+    for h in range(h_v):
+        one = [t.cpu() for t in (q[:, 0], k[:, 0], v[:, h])]
+        O_ref, S_ref = _prompt_reference(*one, g[h].cpu(), torch.zeros(1, d, d), [(0, T)])
+        size, _ = _prompt_reference(*(t.abs() for t in one), g[h].cpu(), torch.zeros(1, d, d), [(0, T)])
+        for S in (S1, S2):
+            assert float((S[0, h].cpu().double() - S_ref[0]).norm()) <= TOL_F32 * float(S_ref[0].norm())
+        assert float((O1[:, h].cpu().double() - O_ref).norm()) <= TOL_F32 * float(O_ref.norm())
+        assert bool(((O2[:, h].cpu().double() - O_ref).abs() <= 2.0 ** -8 * O_ref.abs() + TOL_F32 * size).all())
