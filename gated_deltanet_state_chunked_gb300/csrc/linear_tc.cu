@@ -51,7 +51,7 @@
 // loop is about as long as the chunk; at 64 prompts of 1556 tokens, 16/32 heads, the board's power limit
 // also holds the clock near 1.8 of 2.07 GHz.  Measured there: 605 us, 4.0 TB/s of 2.45 GB (665 us and
 // 4.1 TB/s with entering states; up to 717 us on boards that are held lower); one prompt of 3,277 tokens
-// 54 us, of 32,768 state only 115 us.  Measured and left at that first shape: QS issued by the KV warp
+// 55 us, of 32,768 state only 115 us (an SM has work for 75% of that, its tensor pipe for 65% of its work).  Measured and left at that first shape: QS issued by the KV warp
 // (640 to 690 us) or by the work's warp (683), PV before QS (787), outputs stored from registers (700),
 // outputs staged in Q's tile (647), other register shares (609 to 689).
 #include <cuda.h>
@@ -274,6 +274,11 @@ __device__ __forceinline__ void amend_outputs(const LinearWork& p, const NanRows
   const size_t v_at = (size_t)s.t_begin * v_step + (size_t)h * p.d_v + d;
   const size_t k_at = (size_t)s.t_begin * k_step + (size_t)(h / (p.h_v / p.h_k)) * p.d_k + 4 * lane;
   const uint16_t* v = static_cast<const uint16_t*>(p.v) + v_at;
+  const ItemState state = item_state(p, s, h, true);
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (state.S_in && 4 * lane < p.d_k) S = *reinterpret_cast<const float4*>(state.S_in + (size_t)d * p.d_k + 4 * lane);
+  // (no output of a row that enters with infinities or NaN is finite)
+  if (__any_sync(0xffffffffu, !isfinite(S.x) || !isfinite(S.y) || !isfinite(S.z) || !isfinite(S.w))) return;
   int first = s.len;  // the first such token
 #pragma unroll 1
   for (int t0 = 0; t0 < s.len && first == s.len; t0 += 32) {
@@ -288,16 +293,17 @@ __device__ __forceinline__ void amend_outputs(const LinearWork& p, const NanRows
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xffff0000u));
   };
-  const ItemState state = item_state(p, s, h, true);
-  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (state.S_in && 4 * lane < p.d_k) S = *reinterpret_cast<const float4*>(state.S_in + (size_t)d * p.d_k + 4 * lane);
   const DecayStep f = decay_step(p.log_decay[h], 1);
-#pragma unroll 1
-  for (int t = 0; t < first; ++t) {
+  auto step = [&](int t) {
     const float x = __uint_as_float((uint32_t)v[t * v_step] << 16);
     const float4 k = four(p.k, t);
     S = make_float4(f(S.x, x * k.x), f(S.y, x * k.y), f(S.z, x * k.z), f(S.w, x * k.w));
-    if (t < begin) continue;
+  };
+#pragma unroll 4
+  for (int t = 0; t < begin; ++t) step(t);
+#pragma unroll 1
+  for (int t = begin; t < first; ++t) {
+    step(t);
     const float4 q = four(p.q, t);
     float o = fmaf(S.x, q.x, fmaf(S.y, q.y, fmaf(S.z, q.z, S.w * q.w)));
 #pragma unroll

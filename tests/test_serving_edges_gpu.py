@@ -142,6 +142,17 @@ def test_prompt_values_that_are_no_numbers_in_many_sequences(dt):
     _check_not_finite(x)
 
 
+@pytest.mark.parametrize("dt", NOT_FINITE_TYPES)
+@pytest.mark.parametrize("decay", [-1e-4, -0.5])
+def test_prompt_late_value_that_is_no_number_in_a_long_sequence(dt, decay):
+    """The outputs computed again carry the state over thousands of tokens."""
+    x = _prompt([4000, 3], 1, 160, 8, 16, dt, 3750)  # (more heads than SMs: not cut)
+    x["log_decay"][:] = decay
+    x["v"][3950, :, 2] = NAN
+    x["v"][3960, 7, 15] = INF
+    _check_not_finite(x, in_place=True)
+
+
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("n", [1, 3])
 @pytest.mark.parametrize("state_only", [False, True])
