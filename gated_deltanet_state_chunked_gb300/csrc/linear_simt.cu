@@ -16,7 +16,7 @@
 // Bound: fp32 arithmetic and the shared-memory reads that feed it.  A chunk of 128 x 128 heads is 2.7 M
 // multiply-adds, 21,300 clocks of an SM's pipes; it takes about 39,000 (P 7,000, Q S 12,700, P V 6,500,
 // S 11,200), with the 8 warps that one CTA's shared memory leaves room for.  24 ragged prompts of 16,411
-// tokens in all (8/16 heads, d_k 96, d_v 120): 465 us (the tiles read without asynchronous copies: 523;
+// tokens in all (8/16 heads, d_k 96, d_v 120): 465 to 495 us on different boards (on the first: the tiles read without asynchronous copies: 523;
 // four multiply-adds where two packed ones are now: 478; rows of P V paired so that every warp has as many
 // tokens, and packed scores: 469 to 471, though 4% less at 128 x 128; one row a thread and no tiles: 3,830).  TF32
 // products on the warp-level tensor cores were not taken: three of them for fp32 accuracy run at 1.36 times
