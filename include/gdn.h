@@ -228,7 +228,7 @@ int gdn_compose(const gdn_dims* dims, int32_t K, const float* const* T, const fl
  * Scratch, from the library's pool and returned to it in stream order: a plan of the call when it has
  * several sequences, and the states between the segments of prompts that are cut to fill the GPU (at
  * most two states of d_v d_k floats per SM; nothing for a single short prompt).  The call can be
- * captured into a graph and replayed with new contents.
+ * captured into a graph and replayed with new contents.  O_out overlaps no input.
  */
 int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
                     const int32_t* cu_seqlens, const float* S0, void* O_out, float* S_out, void* stream);
@@ -256,7 +256,8 @@ int gdn_linear_attn(const gdn_dims* dims, const void* q, const void* k, const vo
  * key-value cache, so it is advanced by exactly the tokens that stand.
  * A slot past the pool, a count outside the window, or a slot that an earlier request of the call
  * already updates: that request is skipped and GDN_ERR_SHAPE reported through gdn_get_status.
- * No scratch memory; the call can be captured into a graph and replayed with new contents.
+ * No scratch memory; the call can be captured into a graph and replayed with new contents.  O_out overlaps
+ * no input.
  */
 int gdn_decode(const gdn_dims* dims, int32_t n_slots, const void* q, const void* k, const void* v, const float* g,
                const float* beta, const int32_t* slots, const int32_t* counts, float* S_pool, void* O_out,
@@ -281,7 +282,7 @@ typedef struct {
  *               the drafts were chosen outright (each with probability 1)
  *   drafted     int32 [n_seqs][n_draft]
  *   draft_lens  int32 [n_seqs], each request's drafts, 0 to n_draft; NULL: n_draft each.  Negative:
- *               padding, nothing of that request is read or written.
+ *               padding, nothing of that request is written, and what it holds does not matter.
  *   uniforms    fp32 [n_seqs][n_draft + 1] in [0, 1): the first n_draft for the drafts, the last one
  *               for the sampled token
  * Request by request: draft j is accepted while u_j * q_j(x_j) < p_j(x_j), in exact arithmetic.  Behind
