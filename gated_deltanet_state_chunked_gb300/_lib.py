@@ -59,6 +59,22 @@ class GdnVerifyDims(ctypes.Structure):
     ]
 
 
+class GdnPagedDims(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("n_seqs", "total_tokens", "max_q", "h_q", "h_kv", "d", "page_size",
+                                                    "n_pages", "table_width", "dtype", "window")] \
+        + [("scale", ctypes.c_float)] \
+        + [(name, ctypes.c_int64) for name in ("table_stride", "q_stride", "k_stride", "v_stride", "k_page", "k_token",
+                                               "k_head", "v_page", "v_token", "v_head")]
+
+
+GDN_MAX_AXES = 4
+
+
+class GdnRotary(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("neighbours", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * GDN_MAX_AXES)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, code: int, where: str, message: str):
         self.code = code
@@ -78,6 +94,8 @@ SIGNATURES = {
     "gdn_linear_attn": ([_PD, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "gdn_decode": ([_PD, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "gdn_verify_draft": ([ctypes.POINTER(GdnVerifyDims), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "gdn_kv_append": ([ctypes.POINTER(GdnPagedDims), ctypes.POINTER(GdnRotary)] + [_VP] * 12, ctypes.c_int),
+    "gdn_paged_attn": ([ctypes.POINTER(GdnPagedDims)] + [_VP] * 9, ctypes.c_int),
     "gdn_get_status": ([_VP], ctypes.c_int),
     "gdn_last_error": ([], ctypes.c_char_p),
     "gdn_workspace_bytes": ([_PD], ctypes.c_size_t),

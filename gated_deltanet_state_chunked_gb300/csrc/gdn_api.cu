@@ -38,6 +38,7 @@ __device__ int g_status;  // sticky per-device status (one copy per device that 
 
 constexpr int kMaxGridY = 65535;    // v-heads of one launch of the prompt and decode kernels
 constexpr int kMaxRows = INT32_MAX - 1023;  // tokens or drafts of a serving call: the kernels step past the last in 32 bits
+constexpr int kMaxGroup = 128;    // query heads that share a key head: the rows of the smallest long-chunk tile
 constexpr int kMaxVocab = 1 << 19;  // sums of 2^-44 fixed-point probabilities are at most 2^63
 
 int check_head_dims(const gdn_dims* d) {
@@ -118,6 +119,66 @@ int check_replay_args(const gdn_dims* dims, const void* q, const void* k, const 
   p->augmented = 0; p->l2norm = (dims->flags & GDN_QK_L2NORM) ? 1 : 0;
   p->write_O = state_only ? 0 : 1; p->scale = dims->scale; p->status = status;
   p->scalar_decay = (dims->flags & GDN_SCALAR_DECAY) ? 1 : 0;
+  return GDN_OK;
+}
+
+// Checks that gdn_kv_append and gdn_paged_attn share: fills *p apart from the call's own tensors, sets
+// *nothing for a call without tokens.
+int check_paged(const gdn_paged_dims* d, const void* q, const void* k, const void* v, const int32_t* table,
+                const int32_t* kv_lens, const int32_t* cu, PagedParams* p, bool* nothing) {
+  g_last_error.clear();
+  *nothing = false;
+  if (!d) return fail(GDN_ERR_ARG, "dims is NULL");
+  if (d->n_seqs < 0 || d->total_tokens < 0) return fail(GDN_ERR_ARG, "negative n_seqs or total_tokens");
+  if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d", d->dtype);
+  if (d->h_q <= 0 || d->h_kv <= 0) return fail(GDN_ERR_ARG, "h_q and h_kv must be positive");
+  if (d->h_q % d->h_kv != 0) return fail(GDN_ERR_SHAPE, "h_q (%d) must be a multiple of h_kv (%d)", d->h_q, d->h_kv);
+  if (d->h_q / d->h_kv > kMaxGroup || d->h_q > kMaxGridY)
+    return fail(GDN_ERR_UNSUPPORTED, "h_q=%d, h_kv=%d: at most %d query heads to a key head, %d in all", d->h_q, d->h_kv,
+                kMaxGroup, kMaxGridY);
+  if (d->d <= 0 || d->d > kMaxHead || d->d % 8)
+    return fail(GDN_ERR_UNSUPPORTED, "d=%d: need a multiple of 8 in [8, %d]", d->d, kMaxHead);
+  if (d->max_q < 1) return fail(GDN_ERR_ARG, "max_q must be at least 1");
+  if (d->page_size <= 0 || (d->page_size & (d->page_size - 1)))
+    return fail(GDN_ERR_UNSUPPORTED, "page_size=%d must be a power of two", d->page_size);
+  if (d->n_pages < 0 || d->table_width < 0 || d->window < 0) return fail(GDN_ERR_ARG, "negative n_pages, table_width or window");
+  if (d->total_tokens > kMaxRows) return fail(GDN_ERR_UNSUPPORTED, "total_tokens=%d above %d", d->total_tokens, kMaxRows);
+  if ((long long)d->table_width * d->page_size > kMaxRows)
+    return fail(GDN_ERR_UNSUPPORTED, "a table of %d pages of %d tokens: at most %d tokens", d->table_width, d->page_size, kMaxRows);
+  if (d->table_stride < d->table_width) return fail(GDN_ERR_SHAPE, "table_stride is below table_width (%d)", d->table_width);
+  if (d->n_seqs == 0 || d->total_tokens == 0) {
+    *nothing = true;
+    return GDN_OK;
+  }
+  if (!cu && d->total_tokens % d->n_seqs)
+    return fail(GDN_ERR_SHAPE, "without cu_seqlens total_tokens (%d) must be n_seqs (%d) windows of one length",
+                d->total_tokens, d->n_seqs);
+  if (!cu && d->total_tokens / d->n_seqs > d->max_q)
+    return fail(GDN_ERR_SHAPE, "windows of %d tokens, max_q is %d", d->total_tokens / d->n_seqs, d->max_q);
+  if (!kv_lens || !k || !v || (!table && d->table_width > 0))
+    return fail(GDN_ERR_ARG, "k, v, page_table and kv_lens are required");
+  const int64_t unit = d->dtype == GDN_BF16 ? 8 : 4;
+  const int64_t steps[] = {d->k_page, d->k_token, d->k_head, d->v_page, d->v_token, d->v_head};
+  for (const int64_t s : steps) {
+    if (s < 0) return fail(GDN_ERR_ARG, "a negative stride of the pages");
+    if (s % unit) return fail(GDN_ERR_ALIGN, "strides of the pages must be multiples of 16 bytes");
+  }
+  if (q && d->q_stride < (int64_t)d->h_q * d->d) return fail(GDN_ERR_SHAPE, "q_stride is below h_q * d");
+  if (q && d->q_stride % unit) return fail(GDN_ERR_ALIGN, "q_stride must be a multiple of 16 bytes");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16)) return fail(GDN_ERR_ALIGN, "q, k and v must be 16-byte aligned");
+  if (!aligned(table, 4) || !aligned(kv_lens, 4) || !aligned(cu, 4))
+    return fail(GDN_ERR_ALIGN, "page_table, kv_lens and cu_seqlens must be 4-byte aligned");
+  *p = PagedParams{};
+  p->q = q; p->k = k; p->v = v; p->table = table; p->kv_lens = kv_lens; p->cu = cu;
+  p->table_stride = d->table_stride; p->q_stride = d->q_stride; p->k_stride = d->k_stride; p->v_stride = d->v_stride;
+  p->k_page = d->k_page; p->k_token = d->k_token; p->k_head = d->k_head;
+  p->v_page = d->v_page; p->v_token = d->v_token; p->v_head = d->v_head;
+  p->n = d->n_seqs; p->total = d->total_tokens; p->max_q = d->max_q; p->h_q = d->h_q; p->h_kv = d->h_kv;
+  p->group = d->h_q / d->h_kv; p->d = d->d; p->n_pages = d->n_pages; p->width = d->table_width; p->window = d->window;
+  while ((1 << p->page_shift) < d->page_size) ++p->page_shift;
+  p->scale = d->scale;
+  p->status = device_status_word();
+  if (!p->status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   return GDN_OK;
 }
 
@@ -401,6 +462,81 @@ int gdn_verify_draft(const gdn_verify_dims* dims, const void* target, const void
   if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   const cudaError_t e = launch_verify(p, dims->dtype == GDN_BF16, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gdn_verify_draft launch");
+  return GDN_OK;
+}
+
+int gdn_kv_append(const gdn_paged_dims* dims, const gdn_rotary* rotary, const void* q, const void* k, const void* v,
+                  const float* inv_freq, const int32_t* positions, const int32_t* page_table, const int32_t* kv_lens,
+                  const int32_t* cu_seqlens, void* k_pages, void* v_pages, void* q_out, void* stream) {
+  PagedParams p;
+  bool nothing = false;
+  const int rc = check_paged(dims, q, k, v, page_table, kv_lens, cu_seqlens, &p, &nothing);
+  if (rc) return rc;
+  const int64_t unit = dims->dtype == GDN_BF16 ? 8 : 4;
+  const int64_t least = (int64_t)dims->h_kv * dims->d;
+  if (rotary && rotary->rotary_dim) {
+    if (rotary->rotary_dim < 0 || rotary->rotary_dim % 2 || rotary->rotary_dim > dims->d)
+      return fail(GDN_ERR_UNSUPPORTED, "rotary_dim=%d: need an even number up to d (%d)", rotary->rotary_dim, dims->d);
+    if (rotary->n_axes < 1 || rotary->n_axes > GDN_MAX_AXES)
+      return fail(GDN_ERR_UNSUPPORTED, "n_axes=%d outside [1, %d]", rotary->n_axes, GDN_MAX_AXES);
+    if (rotary->neighbours != 0 && rotary->neighbours != 1) return fail(GDN_ERR_ARG, "neighbours is 0 or 1");
+    p.rotary = rotary->rotary_dim; p.neighbours = rotary->neighbours; p.n_axes = rotary->n_axes;
+    if (p.n_axes > 1) {
+      long long pairs = 0;
+      for (int i = 0; i < p.n_axes; ++i) {
+        if (rotary->sections[i] < 0) return fail(GDN_ERR_ARG, "a negative section");
+        pairs += p.sections[i] = rotary->sections[i];
+      }
+      if (pairs != p.rotary / 2)
+        return fail(GDN_ERR_SHAPE, "sections of %lld pairs, rotary_dim %d has %d", pairs, p.rotary, p.rotary / 2);
+    }
+  }
+  if (nothing) return GDN_OK;
+  if (!k_pages || !v_pages) {
+    if (dims->n_pages > 0) return fail(GDN_ERR_ARG, "k_pages and v_pages are required");
+  }
+  if ((q == nullptr) != (q_out == nullptr)) return fail(GDN_ERR_ARG, "q and q_out go together");
+  if (p.rotary && !inv_freq) return fail(GDN_ERR_ARG, "inv_freq is required");
+  if (p.rotary && p.n_axes > 1 && !positions) return fail(GDN_ERR_ARG, "positions are required for several axes");
+  if (dims->k_stride < least || dims->v_stride < least) return fail(GDN_ERR_SHAPE, "k_stride or v_stride is below h_kv * d");
+  if (dims->k_stride % unit || dims->v_stride % unit) return fail(GDN_ERR_ALIGN, "k_stride and v_stride must be multiples of 16 bytes");
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(q_out, 16))
+    return fail(GDN_ERR_ALIGN, "k_pages, v_pages and q_out must be 16-byte aligned");
+  if (!aligned(inv_freq, 4) || !aligned(positions, 4)) return fail(GDN_ERR_ALIGN, "inv_freq and positions must be 4-byte aligned");
+  if (q && q == q_out && dims->q_stride != (int64_t)dims->h_q * dims->d)
+    return fail(GDN_ERR_ARG, "q_out may be q only where q has no gaps");
+  p.inv_freq = inv_freq; p.positions = positions; p.k_pages = k_pages; p.v_pages = v_pages; p.O = q_out;
+  const cudaError_t e = launch_kv_append(p, dims->dtype == GDN_BF16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv_append launch");
+  return GDN_OK;
+}
+
+int gdn_paged_attn(const gdn_paged_dims* dims, const void* q, const void* k_pages, const void* v_pages,
+                   const int32_t* page_table, const int32_t* kv_lens, const int32_t* cu_seqlens, void* O_out,
+                   float* lse_out, void* stream) {
+  PagedParams p;
+  bool nothing = false;
+  int rc = check_paged(dims, q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, &p, &nothing);
+  if (rc || nothing) return rc;
+  if (!q || !O_out) return fail(GDN_ERR_ARG, "q and O_out are required");
+  if (!aligned(O_out, 16)) return fail(GDN_ERR_ALIGN, "O_out must be 16-byte aligned");
+  if (!aligned(lse_out, 4)) return fail(GDN_ERR_ALIGN, "lse_out must be 4-byte aligned");
+  p.O = O_out; p.lse = lse_out;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int bf16 = dims->dtype == GDN_BF16;
+  size_t bytes = 0;
+  void* ws = nullptr;
+  cudaError_t e = paged_workspace_bytes(p, bf16, &bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_paged_attn set-up");
+  cudaMemPool_t pool = nullptr;
+  rc = scratch_pool(&pool);
+  if (rc) return rc;
+  e = cudaMallocFromPoolAsync(&ws, bytes, pool, st);
+  if (e != cudaSuccess) return fail(GDN_ERR_NOMEM, "scratch of %zu bytes: %s", bytes, cudaGetErrorString(e));
+  e = launch_paged_attn(p, bf16, ws, st);
+  const cudaError_t ef = cudaFreeAsync(ws, st);
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_paged_attn launch");
+  if (ef != cudaSuccess) return cuda_fail(ef, "scratch release");
   return GDN_OK;
 }
 

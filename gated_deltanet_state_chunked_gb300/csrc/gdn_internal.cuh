@@ -177,6 +177,31 @@ struct VerifyParams {
 };
 cudaError_t launch_verify(const VerifyParams& p, int bf16, cudaStream_t stream);
 
+// Paged key-value cache (gdn_kv_append, gdn_paged_attn).
+struct PagedParams {
+  const void* q;
+  const void* k;  // gdn_kv_append: the new keys and values; gdn_paged_attn: the pages
+  const void* v;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int32_t* cu;  // or null: total / n tokens each
+  void* O;            // gdn_kv_append: the rotated queries
+  float* lse;         // or null
+  void* k_pages;      // gdn_kv_append
+  void* v_pages;
+  const float* inv_freq;
+  const int32_t* positions;  // or null
+  int* status;
+  int64_t table_stride, q_stride, k_stride, v_stride, k_page, k_token, k_head, v_page, v_token, v_head;
+  int n, total, max_q, h_q, h_kv, group, d, page_shift, n_pages, width, window;
+  float scale;
+  int rotary, neighbours, n_axes, sections[GDN_MAX_AXES];
+};
+cudaError_t launch_kv_append(const PagedParams& p, int bf16, cudaStream_t stream);
+// Scratch that a call needs on the current device, and the call.
+cudaError_t paged_workspace_bytes(const PagedParams& p, int bf16, size_t* bytes);
+cudaError_t launch_paged_attn(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream);
+
 // Sticky status word of the current device (device pointer).
 int* device_status_word();
 

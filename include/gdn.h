@@ -304,6 +304,88 @@ int gdn_verify_draft(const gdn_verify_dims* dims, const void* target, const void
                      const int32_t* draft_lens, const float* uniforms, int32_t* counts_out, int32_t* tokens_out,
                      void* stream);
 
+typedef struct {
+  int32_t n_seqs;        /* requests */
+  int32_t total_tokens;  /* rows of q, k, v and O: the requests' new tokens */
+  int32_t max_q;         /* most new tokens of one request, at least 1 */
+  int32_t h_q;           /* query heads, a multiple of h_kv: query head h reads key head h / (h_q / h_kv) */
+  int32_t h_kv;          /* key and value heads */
+  int32_t d;             /* head dim of queries, keys and values: a multiple of 8, at most 128 */
+  int32_t page_size;     /* tokens of a page, a power of two */
+  int32_t n_pages;       /* pages of the cache */
+  int32_t table_width;   /* entries of a request's row of the page table */
+  int32_t dtype;         /* of q, k, v, the pages and O: GDN_F32 or GDN_BF16 */
+  int32_t window;        /* gdn_paged_attn: a token sees the last `window` tokens, itself among them; 0: all */
+  float scale;           /* gdn_paged_attn: multiplies q.k */
+  int64_t table_stride;  /* elements between the rows of the page table, at least table_width */
+  int64_t q_stride, k_stride, v_stride; /* elements between the tokens of q, and of the new k and v (a token's heads
+                                           lie one after another) */
+  int64_t k_page, k_token, k_head; /* elements between the pages, a page's tokens and a token's heads of k_pages */
+  int64_t v_page, v_token, v_head; /* the same of v_pages */
+} gdn_paged_dims;
+
+#define GDN_MAX_AXES 4
+typedef struct {
+  int32_t rotary_dim; /* values of a head that are rotated (the first ones): even, at most d; 0: none */
+  int32_t neighbours; /* 0: values i and i + rotary_dim / 2 turn together; 1: values 2 i and 2 i + 1 */
+  int32_t n_axes;     /* rows of positions, 1 to GDN_MAX_AXES */
+  int32_t sections[GDN_MAX_AXES]; /* consecutive pairs that turn by each axis, rotary_dim / 2 in all (not read for one axis) */
+} gdn_rotary;
+
+/*
+ * gdn_kv_append -- new keys and values into a paged cache, rotated by their positions on the way.
+ * The attention layers between a hybrid model's recurrent ones; the pages name their cache (its
+ * copy beside the replay is "Tail-Replay: ..." section 3) and give no kernel.
+ *   k, v          [total_tokens][h_kv][d] in `dims->dtype`, k_stride and v_stride apart
+ *   page_table    int32 device [n_seqs][table_width]: position p of request i lies in page page_table[i][p /
+ *                 page_size], slot p % page_size.  Entries behind a request's length are not read.
+ *   kv_lens       int32 device [n_seqs]: tokens in the cache once the call's are in it; new token t of n takes
+ *                 position kv_lens - n + t, and one whose position is below zero has no place (nothing is written
+ *                 for it).  Negative: padding, nothing of that request is read or written.
+ *   cu_seqlens    int32 device [n_seqs + 1], or NULL: every request has total_tokens / n_seqs new tokens
+ *   k_pages, v_pages  the cache; written at the new tokens' places alone
+ *   q, q_out      queries to rotate by the same positions, [total_tokens][h_q][d] q_stride apart, into
+ *                 [total_tokens][h_q][d] without gaps; both NULL: none.  q_out may be q where q has no gaps.
+ *   rotary        NULL: k and q are copied as they are
+ *   inv_freq      fp32 device [rotary_dim / 2]: pair i turns by the angle position * inv_freq[i]
+ *   positions     int32 device [n_axes][total_tokens], or NULL (one axis): a token's place in the cache
+ * A pair (a, b) becomes (a cos - b sin, b cos + a sin).  Angles are reduced in fp64, so that far positions
+ * lose nothing; the rest is fp32 and rounded once to `dtype`.
+ * A malformed range (as in gdn_replay), one of more than max_q tokens, a kv_lens past the table, or a page
+ * outside the cache: the request (for a page, the tokens of that page) is skipped and GDN_ERR_SHAPE reported through
+ * gdn_get_status.  No scratch memory; the call can be captured into a graph and replayed with new contents.  The pages overlap
+ * neither q, k, v nor q_out; two tokens of a call never have the same place.
+ * Alignment: 16 bytes for q, k, v, the pages, q_out and each of the strides.
+ */
+int gdn_kv_append(const gdn_paged_dims* dims, const gdn_rotary* rotary, const void* q, const void* k, const void* v,
+                  const float* inv_freq, const int32_t* positions, const int32_t* page_table, const int32_t* kv_lens,
+                  const int32_t* cu_seqlens, void* k_pages, void* v_pages, void* q_out, void* stream);
+
+/*
+ * gdn_paged_attn -- attention of each request's new tokens over its paged cache: one token, a window of
+ * drafts, or a chunk of a prompt.
+ *     o_t = sum_j p_tj v_j,   p_tj = exp(scale q_t.k_j - lse_t),   lse_t = log sum_j exp(scale q_t.k_j)
+ * over the keys j that token t sees: with kv_lens tokens in the cache, the n new ones the last of them
+ * (gdn_kv_append has put them there), token t of n has position p = kv_lens - n + t and sees 0 <= j <= p, and
+ * with a window only j > p - window.
+ *   q, page_table, kv_lens, cu_seqlens, the pages: as in gdn_kv_append
+ *   O_out         [total_tokens][h_q][d] in `dims->dtype`, without gaps
+ *   lse_out       fp32 [total_tokens][h_q], or NULL
+ * A token that sees no key (its position is below zero) has output 0 and lse -inf.  Rows outside every range, and
+ * those of padding (kv_lens negative), are left as they were.  What lies in the cache behind a request's length is
+ * not read, and an infinite or NaN key or value reaches only the tokens that see it.
+ * Sums are fp32.  bf16: the weights p are rounded once to bf16 as operands of the sum over values, as the output
+ * itself is: together 2.4e-3 of an output's norm, where its own rounding alone is 1.7e-3; lse has neither.
+ * Malformed ranges and lengths are reported as by gdn_kv_append, the request's rows left as they were; with a page
+ * outside the cache the request's outputs are unspecified.
+ * Scratch, from the library's pool and returned to it in stream order: partial results of requests that are shared
+ * between SMs, at most two tiles of d floats for each row per SM.  The call can be captured into a graph and
+ * replayed with new contents.  O_out and lse_out overlap no input.
+ */
+int gdn_paged_attn(const gdn_paged_dims* dims, const void* q, const void* k_pages, const void* v_pages,
+                   const int32_t* page_table, const int32_t* kv_lens, const int32_t* cu_seqlens, void* O_out,
+                   float* lse_out, void* stream);
+
 /*
  * gdn_get_status -- synchronise `stream`, then return and clear the sticky
  * device status of the current device: GDN_OK, GDN_ERR_SHAPE (a malformed
