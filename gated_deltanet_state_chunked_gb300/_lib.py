@@ -75,6 +75,16 @@ class GdnRotary(ctypes.Structure):
                 ("sections", ctypes.c_int32 * GDN_MAX_AXES)]
 
 
+class GdnBeamDims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("beams", ctypes.c_int32), ("best", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("stride", ctypes.c_int64)]
+
+
+class GdnReorderDims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("beams", ctypes.c_int32), ("n_slots", ctypes.c_int32), ("layers", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("layer_stride", ctypes.c_int64)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, code: int, where: str, message: str):
         self.code = code
@@ -96,6 +106,8 @@ SIGNATURES = {
     "gdn_verify_draft": ([ctypes.POINTER(GdnVerifyDims), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
     "gdn_kv_append": ([ctypes.POINTER(GdnPagedDims), ctypes.POINTER(GdnRotary)] + [_VP] * 12, ctypes.c_int),
     "gdn_paged_attn": ([ctypes.POINTER(GdnPagedDims)] + [_VP] * 9, ctypes.c_int),
+    "gdn_beam_select": ([ctypes.POINTER(GdnBeamDims)] + [_VP] * 6, ctypes.c_int),
+    "gdn_beam_reorder": ([ctypes.POINTER(GdnReorderDims)] + [_VP] * 5, ctypes.c_int),
     "gdn_get_status": ([_VP], ctypes.c_int),
     "gdn_last_error": ([], ctypes.c_char_p),
     "gdn_workspace_bytes": ([_PD], ctypes.c_size_t),

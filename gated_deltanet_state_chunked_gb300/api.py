@@ -483,6 +483,68 @@ def gdn_paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *,
                    v_pages.data_ptr(), *tables)[0]
 
 
+def gdn_beam_select(logits, scores, best=None, *, scores_out=None, parents_out=None, tokens_out=None, stream=None):
+    """The ``best`` (None: as many as beams) continuations of each request over its beams and the vocabulary (see
+    gdn.h): the largest scores + log softmax(logits); of equal ones the lower beam's, then the lower token.
+
+    logits: [n, beams, vocab] fp32 or bf16 (evenly spaced rows; a vocabulary slice of padded rows will do); scores:
+    fp32 [n, beams], -inf for a dead beam.  Returns (scores, parents, tokens), [n, best] fp32, int32, int32, largest
+    first; -inf, -1, -1 where there are fewer continuations."""
+    lib = _lib.load()
+    if logits.dim() != 3:
+        raise ValueError("logits must be [n, beams, vocab]")
+    n, beams, vocab = logits.shape
+    dt = logits.dtype
+    if dt not in _DTYPE:
+        raise ValueError(f"unsupported dtype {dt}")
+    best = beams if best is None else best
+    _fits(n, vocab, best)
+    dev = _cuda_index("logits", logits)
+    stride = _prob_rows("logits", logits, (n, beams, vocab))
+    out, i32 = (n, best), torch.int32
+    s_ptr = _want("scores", scores, dev, torch.float32, (n, beams))
+    _want("scores_out", scores_out, dev, torch.float32, out)
+    _want("parents_out", parents_out, dev, i32, out)
+    _want("tokens_out", tokens_out, dev, i32, out)
+    dims = _lib.GdnBeamDims(n, beams, best, vocab, _DTYPE[dt], stride)
+    return tuple(_launch(lib.gdn_beam_select, "gdn_beam_select", logits, stream,
+                         ((out, torch.float32) if scores_out is None else scores_out,
+                          (out, i32) if parents_out is None else parents_out,
+                          (out, i32) if tokens_out is None else tokens_out), dims, logits.data_ptr(), s_ptr))
+
+
+def gdn_beam_reorder(pool, slots, parents, *, layers=False, slots_out=None, stream=None):
+    """The rows of ``pool`` follow their beams, in place (see gdn.h): the first child of a beam keeps its parent's
+    row, the others get copies in the rows of beams without children.
+
+    pool: [n_slots, ...], or [n_layers, n_slots, ...] with ``layers`` (all layers move alike), any dtype, rows of a
+    multiple of 16 bytes, each row contiguous; slots, parents: int32 [n, beams] on the device (a negative first slot:
+    padding; a negative parent: the new beam continues none).  Returns the new beams' slots, int32 [n, beams] (-1 for
+    padding)."""
+    lib = _lib.load()
+    lead = 2 if layers else 1
+    if pool.dim() < lead or slots.dim() != 2:
+        raise ValueError("pool must be [n_slots, ...] ([n_layers, n_slots, ...] with layers) and slots [n, beams]")
+    n_layers, n_slots = pool.shape[:2] if layers else (1, pool.shape[0])
+    n, beams = slots.shape
+    _fits(n, beams, n_slots, n_layers)
+    dev = _cuda_index("pool", pool)
+    size = pool.element_size()
+    row, steps = 1, pool.stride()
+    for length, step in zip(reversed(pool.shape[lead:]), reversed(steps[lead:])):
+        if length != 1 and step != row:
+            raise ValueError("pool: each row must be contiguous")
+        row *= length
+    slot_step = steps[lead - 1] if n_slots > 1 else row
+    layer_step = steps[0] if layers and n_layers > 1 else row
+    i32 = torch.int32
+    args = (_want("slots", slots, dev, i32, (n, beams)), _want("parents", parents, dev, i32, (n, beams)))
+    _want("slots_out", slots_out, dev, i32, (n, beams))
+    dims = _lib.GdnReorderDims(n, beams, n_slots, n_layers, row * size, slot_step * size, layer_step * size)
+    return _launch(lib.gdn_beam_reorder, "gdn_beam_reorder", pool, stream,
+                   (((n, beams), i32) if slots_out is None else slots_out,), dims, *args, pool.data_ptr())[0]
+
+
 def gdn_get_status(stream=None, device=None):
     """Synchronise the stream; raise GdnError if the device recorded an error."""
     lib = _lib.load()

@@ -540,6 +540,80 @@ int gdn_paged_attn(const gdn_paged_dims* dims, const void* q, const void* k_page
   return GDN_OK;
 }
 
+int gdn_beam_select(const gdn_beam_dims* dims, const void* logits, const float* scores, float* scores_out,
+                    int32_t* parents_out, int32_t* tokens_out, void* stream) {
+  g_last_error.clear();
+  if (!dims) return fail(GDN_ERR_ARG, "dims is NULL");
+  if (dims->n_seqs < 0) return fail(GDN_ERR_ARG, "negative n_seqs");
+  if (dims->beams <= 0 || dims->best <= 0 || dims->vocab <= 0) return fail(GDN_ERR_ARG, "beams, best and vocab must be positive");
+  if (dims->dtype != GDN_F32 && dims->dtype != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "dtype %d", dims->dtype);
+  if (dims->beams > kMaxBeams || dims->best > kMaxBeams)
+    return fail(GDN_ERR_UNSUPPORTED, "beams=%d, best=%d: at most %d", dims->beams, dims->best, kMaxBeams);
+  if (dims->vocab > kMaxVocab) return fail(GDN_ERR_UNSUPPORTED, "vocab=%d above %d", dims->vocab, kMaxVocab);
+  // (a launch has a block for each slice, of 2,048 entries or more unless it is a row's last)
+  if ((long long)dims->n_seqs * dims->beams * ((dims->vocab - 1) / 2048 + 1) > INT32_MAX)
+    return fail(GDN_ERR_UNSUPPORTED, "n_seqs=%d, beams=%d, vocab=%d: too many pieces of work", dims->n_seqs, dims->beams, dims->vocab);
+  if (dims->stride < dims->vocab) return fail(GDN_ERR_SHAPE, "the row stride is below vocab (%d)", dims->vocab);
+  if (dims->n_seqs == 0) return GDN_OK;
+  if (!logits || !scores || !scores_out || !parents_out || !tokens_out)
+    return fail(GDN_ERR_ARG, "logits, scores, scores_out, parents_out and tokens_out are required");
+  if (!aligned(logits, dims->dtype == GDN_BF16 ? 2 : 4)) return fail(GDN_ERR_ALIGN, "logits must be aligned to their type");
+  if (!aligned(scores, 4) || !aligned(scores_out, 4) || !aligned(parents_out, 4) || !aligned(tokens_out, 4))
+    return fail(GDN_ERR_ALIGN, "scores, scores_out, parents_out and tokens_out must be 4-byte aligned");
+  if (scores == scores_out) return fail(GDN_ERR_ARG, "scores_out aliases scores");
+  BeamParams p{};
+  p.logits = logits; p.scores = scores; p.scores_out = scores_out; p.parents = parents_out; p.tokens = tokens_out;
+  p.stride = dims->stride; p.n = dims->n_seqs; p.beams = dims->beams; p.best = dims->best; p.vocab = dims->vocab;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  size_t bytes = 0;
+  void* ws = nullptr;
+  cudaError_t e = beam_workspace_bytes(p, &bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_beam_select set-up");
+  cudaMemPool_t pool = nullptr;
+  const int rc = scratch_pool(&pool);
+  if (rc) return rc;
+  e = cudaMallocFromPoolAsync(&ws, bytes, pool, st);
+  if (e != cudaSuccess) return fail(GDN_ERR_NOMEM, "scratch of %zu bytes: %s", bytes, cudaGetErrorString(e));
+  e = launch_beam_select(p, dims->dtype == GDN_BF16, ws, st);
+  const cudaError_t ef = cudaFreeAsync(ws, st);
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_beam_select launch");
+  if (ef != cudaSuccess) return cuda_fail(ef, "scratch release");
+  return GDN_OK;
+}
+
+int gdn_beam_reorder(const gdn_reorder_dims* dims, const int32_t* slots, const int32_t* parents, void* pool,
+                     int32_t* slots_out, void* stream) {
+  g_last_error.clear();
+  if (!dims) return fail(GDN_ERR_ARG, "dims is NULL");
+  if (dims->n_seqs < 0 || dims->n_slots < 0 || dims->layers < 0 || dims->row_bytes < 0)
+    return fail(GDN_ERR_ARG, "negative n_seqs, n_slots, layers or row_bytes");
+  if (dims->beams <= 0) return fail(GDN_ERR_ARG, "beams must be positive");
+  if (dims->beams > kMaxBeams) return fail(GDN_ERR_UNSUPPORTED, "beams=%d: at most %d", dims->beams, kMaxBeams);
+  if ((long long)dims->n_seqs * dims->beams > INT32_MAX || dims->layers > kMaxGridY || dims->row_bytes > (int64_t)kMaxGridY * 65536)
+    return fail(GDN_ERR_UNSUPPORTED, "n_seqs=%d, beams=%d, layers=%d, row_bytes=%lld: more than one launch takes", dims->n_seqs,
+                dims->beams, dims->layers, (long long)dims->row_bytes);
+  if (dims->row_bytes % 16 || dims->slot_stride % 16 || dims->layer_stride % 16)
+    return fail(GDN_ERR_ALIGN, "row_bytes, slot_stride and layer_stride must be multiples of 16");
+  if (dims->n_slots > 1 && dims->slot_stride < dims->row_bytes) return fail(GDN_ERR_SHAPE, "slot_stride is below row_bytes");
+  if (dims->layers > 1 && dims->layer_stride < dims->row_bytes) return fail(GDN_ERR_SHAPE, "layer_stride is below row_bytes");
+  if (dims->n_seqs == 0) return GDN_OK;
+  if (!slots || !parents || !slots_out) return fail(GDN_ERR_ARG, "slots, parents and slots_out are required");
+  if (!pool && dims->n_slots > 0 && dims->layers > 0 && dims->row_bytes > 0) return fail(GDN_ERR_ARG, "pool is required");
+  if (!aligned(pool, 16)) return fail(GDN_ERR_ALIGN, "pool must be 16-byte aligned");
+  if (!aligned(slots, 4) || !aligned(parents, 4) || !aligned(slots_out, 4))
+    return fail(GDN_ERR_ALIGN, "slots, parents and slots_out must be 4-byte aligned");
+  if (slots_out == slots || slots_out == parents) return fail(GDN_ERR_ARG, "slots_out aliases an input");
+  ReorderParams p{};
+  p.pool = static_cast<unsigned char*>(pool); p.slots = slots; p.parents = parents; p.slots_out = slots_out;
+  p.n = dims->n_seqs; p.beams = dims->beams; p.n_slots = dims->n_slots; p.layers = dims->layers;
+  p.row_bytes = dims->layers > 0 ? dims->row_bytes : 0; p.slot_stride = dims->slot_stride; p.layer_stride = dims->layer_stride;
+  p.status = device_status_word();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  const cudaError_t e = launch_beam_reorder(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_beam_reorder launch");
+  return GDN_OK;
+}
+
 int gdn_get_status(void* stream) {
   g_last_error.clear();
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));

@@ -202,6 +202,30 @@ cudaError_t launch_kv_append(const PagedParams& p, int bf16, cudaStream_t stream
 cudaError_t paged_workspace_bytes(const PagedParams& p, int bf16, size_t* bytes);
 cudaError_t launch_paged_attn(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream);
 
+// Beams (gdn_beam_select, gdn_beam_reorder).
+constexpr int kMaxBeams = 64;  // beams of a request, and continuations that are selected
+struct BeamParams {
+  const void* logits;
+  const float* scores;  // [n][beams]
+  float* scores_out;    // [n][best]
+  int32_t* parents;
+  int32_t* tokens;
+  int64_t stride;       // elements between consecutive rows of logits
+  int n, beams, best, vocab;
+};
+cudaError_t beam_workspace_bytes(const BeamParams& p, size_t* bytes);
+cudaError_t launch_beam_select(const BeamParams& p, int bf16, void* workspace, cudaStream_t stream);
+struct ReorderParams {
+  unsigned char* pool;
+  const int32_t* slots;    // [n][beams]
+  const int32_t* parents;  // [n][beams]
+  int32_t* slots_out;      // [n][beams]
+  int* status;
+  int64_t row_bytes, slot_stride, layer_stride;  // bytes
+  int n, beams, n_slots, layers;
+};
+cudaError_t launch_beam_reorder(const ReorderParams& p, cudaStream_t stream);
+
 // Sticky status word of the current device (device pointer).
 int* device_status_word();
 

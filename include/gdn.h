@@ -386,6 +386,60 @@ int gdn_paged_attn(const gdn_paged_dims* dims, const void* q, const void* k_page
                    const int32_t* page_table, const int32_t* kv_lens, const int32_t* cu_seqlens, void* O_out,
                    float* lse_out, void* stream);
 
+typedef struct {
+  int32_t n_seqs;  /* requests */
+  int32_t beams;   /* beams of a request, at most 64 */
+  int32_t best;    /* continuations that are selected, at most 64 */
+  int32_t vocab;   /* entries of a row of logits, at most 524288 */
+  int32_t dtype;   /* of the logits: GDN_F32 or GDN_BF16 */
+  int64_t stride;  /* elements between consecutive rows of logits, at least vocab */
+} gdn_beam_dims;
+
+/*
+ * gdn_beam_select -- the best continuations of each request over its beams and the vocabulary.
+ * The pages have no counterpart; beside gdn_verify_draft, the other way to a request's next tokens.
+ *     total(b, v) = scores[b] + logits[b][v] - log sum_w exp(logits[b][w])
+ *   logits      [n_seqs][beams][vocab] in `dims->dtype`, rows `stride` apart
+ *   scores      fp32 [n_seqs][beams], the beams' totals so far; -inf: the beam is dead
+ *   scores_out, parents_out, tokens_out   fp32, int32, int32 [n_seqs][best]: the `best` largest totals, their
+ *               beams and tokens, largest first; equal totals in the order of their beams, a beam's by
+ *               (larger logit, lower token)
+ * A logit of -inf is never selected, nor is NaN; a row with a NaN or +inf, like a dead beam, has no continuation.
+ * Where there are fewer than `best`, the rest is -inf, -1, -1.  Totals are compared in fp64: the logits' and scores'
+ * numbers as they are, the log sum within 1e-7 of itself; scores_out is rounded once.
+ * Scratch, from the library's pool and returned to it in stream order: 12 + 8 * best bytes for each 16,384 entries
+ * of a row (each 2,048 for few rows).  The call can be captured into a graph.  Outputs overlap no input.
+ */
+int gdn_beam_select(const gdn_beam_dims* dims, const void* logits, const float* scores, float* scores_out,
+                    int32_t* parents_out, int32_t* tokens_out, void* stream);
+
+typedef struct {
+  int32_t n_seqs;   /* requests */
+  int32_t beams;    /* beams of a request, at most 64 */
+  int32_t n_slots;  /* rows of the pool */
+  int32_t layers;   /* pools of the same slots, one after another (one for each layer); 0: slots_out alone */
+  int64_t row_bytes, slot_stride, layer_stride; /* bytes of a row, between rows, between layers: multiples of 16 */
+} gdn_reorder_dims;
+
+/*
+ * gdn_beam_reorder -- the rows of a pool (gdn_decode's states; pages of a key-value cache) follow their beams.
+ * The pages have no counterpart; the call stands between gdn_beam_select and the next gdn_decode.
+ *   slots       int32 device [n_seqs][beams]: the row of each beam so far.  A negative first slot: padding, its
+ *               request's slots_out are -1 and nothing of it moves.
+ *   parents     int32 device [n_seqs][beams]: the beam that each new beam continues, or negative: none (the new beam
+ *               gets a slot, whose row stays as it is)
+ *   pool        any rows of row_bytes, updated in place
+ *   slots_out   int32 device [n_seqs][beams]: the rows of the new beams, a permutation of the request's slots.  The
+ *               first child of a beam keeps its row; the k-th of the other new beams takes the row of the k-th beam
+ *               without children, and its parent's row is copied there.
+ * A slot outside the pool or named twice (by the request, or by an earlier one), or a parent that is no beam: the
+ * request is skipped, its slots_out are -1, and GDN_ERR_SHAPE is reported through gdn_get_status.  No scratch memory;
+ * the call can be captured into a graph and replayed with new contents.  slots_out overlaps no input.  The pool is
+ * 16-byte aligned.
+ */
+int gdn_beam_reorder(const gdn_reorder_dims* dims, const int32_t* slots, const int32_t* parents, void* pool,
+                     int32_t* slots_out, void* stream);
+
 /*
  * gdn_get_status -- synchronise `stream`, then return and clear the sticky
  * device status of the current device: GDN_OK, GDN_ERR_SHAPE (a malformed
