@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s
         if (!whole) s.stat[slot + r] = float2{m[i], l[i]};
         else if (p.lse) p.lse[out] = row_lse(m[i], l[i], sees);
       }
-      if (!fine) again[r] = 1;  // (any of the row's threads)
+      if (!fine && worth_again(l[i])) again[r] = 1;  // (any of the row's threads)
     }
     __syncthreads();
     for (int r = warp; r < BM; r += NT / 32)

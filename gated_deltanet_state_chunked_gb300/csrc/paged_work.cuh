@@ -246,43 +246,67 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void store_f(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
 
-// One row by itself, key by key, over the keys [lo, hi) that it sees: what an infinite or NaN value at a
-// key that the row does not see, but its tile does, has left of it (0 * inf) is computed again, and so are rows whose
-// unnormalised sum is past fp32.  One warp; lane l holds values l, l + 32, ... of the normalised row.
+// 16 bytes of a row of the pages or of q, as fp32 numbers.
+__device__ __forceinline__ void load16(const float* p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+// One row by itself, over the keys [lo, hi) that it sees, for rows whose output a tile leaves infinite or NaN
+// though their sum of weights is a number: an infinite or NaN value at a key that the row does not see, but
+// its tile does, has done that (0 * inf), or an unnormalised sum past fp32, or a value that the row does see.  The
+// maximum and sum first, then the sum of values with weights that add up to 1.  One warp; lane l returns values l, l + 32, ...
 template <typename T>
 __device__ __noinline__ void row_again(const PagedParams& p, int req, int head, int h, int row, int lo, int hi, float (&o)[4],
                                        float* m_out, float* l_out) {
+  constexpr int VEC = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   const T* q = static_cast<const T*>(p.q) + (int64_t)row * p.q_stride + (int64_t)h * p.d;
   const T* kp = static_cast<const T*>(p.k) + head * p.k_head;
   const T* vp = static_cast<const T*>(p.v) + head * p.v_head;
   const int mask = (1 << p.page_shift) - 1;
   const float s2 = p.scale * kLog2e;
-  double acc[4] = {0., 0., 0., 0.};
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int j0 = lo; j0 < hi; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -CUDART_INF_F;
-    int page = -1;
-    if (j < hi) {
-      page = page_of(p, req, j);
-      if (page >= 0) {
-        const T* k = kp + page * p.k_page + (int64_t)(j & mask) * p.k_token;
-        s = 0.f;
-        for (int x = 0; x < p.d; ++x) s = fmaf(to_f(q[x]), to_f(k[x]), s);
-        s *= s2;
-      }
-    }
-    float top = s;
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float m_new = fmaxf(m, top), ref = m_new == -CUDART_INF_F ? 0.f : m_new;
-    const float e = page >= 0 ? exp2f(s - ref) : 0.f, shrink = exp2f(m - ref);
-    float sum = e;
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * shrink + sum;
-    m = m_new;
+  auto score = [&](int j, int* page) {
+    *page = j < hi ? page_of(p, req, j) : -1;
+    if (*page < 0) return -CUDART_INF_F;
+    const T* k = kp + *page * p.k_page + (int64_t)(j & mask) * p.k_token;
+    float s = 0.f;
+    for (int x = 0; x < p.d; x += VEC) {
+      float a[VEC], b[VEC];
+      load16(q + x, a);
+      load16(k + x, b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] *= shrink;
+      for (int i = 0; i < VEC; ++i) s = fmaf(a[i], b[i], s);
+    }
+    return s * s2;
+  };
+  float m = -CUDART_INF_F, l = 0.f;
+  for (int j0 = lo; j0 < hi; j0 += 32) {  // (a lane's own maximum and sum)
+    int page;
+    const float s = score(j0 + lane, &page), m_new = fmaxf(m, s), ref = m_new == -CUDART_INF_F ? 0.f : m_new;
+    l = l * exp2f(m - ref) + (page >= 0 ? exp2f(s - ref) : 0.f);
+    m = m_new;
+  }
+  float top = m;
+  for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  const float ref = top == -CUDART_INF_F ? 0.f : top;
+  l *= exp2f(m - ref);
+  for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  const float f = 1.f / l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = 0.f;
+  for (int j0 = lo; j0 < hi; j0 += 32) {
+    int page;
+    const float s = score(j0 + lane, &page), e = exp2f(s - ref) * f;
     for (int x = 0; x < min(32, hi - j0); ++x) {
       const float w = __shfl_sync(0xffffffffu, e, x);
       const int pg = __shfl_sync(0xffffffffu, page, x);
@@ -290,14 +314,15 @@ __device__ __noinline__ void row_again(const PagedParams& p, int req, int head, 
       const T* v = vp + pg * p.v_page + (int64_t)((j0 + x) & mask) * p.v_token;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.d) acc[i] += (double)w * (double)to_f(v[lane + 32 * i]);
+        if (lane + 32 * i < p.d) o[i] = fmaf(w, to_f(v[lane + 32 * i]), o[i]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = (float)(acc[i] / (double)l);
-  *m_out = m;
+  *m_out = top;
   *l_out = l;
 }
+// Whether a row with such an output is worth it (l: its sum of weights): with a NaN or infinite score every value is
+// NaN already, as with no weight at all.
+__device__ __forceinline__ bool worth_again(float l) { return l > 0.f && l <= 3.402823466e38f; }
 
 // Row r of a tile of item (head, tile): its token of the request and its query head.
 struct Row {
@@ -345,6 +370,8 @@ __device__ __forceinline__ void redo_row(const PagedParams& p, const Scratch& s,
 cudaError_t launch_join(const PagedParams& p, int bf16, const Scratch& s, int G, int BM, int tile_tokens, cudaStream_t stream);
 cudaError_t launch_simt(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream);
 cudaError_t simt_workspace(const PagedParams& p, int bf16, size_t* bytes);
+cudaError_t launch_tc(const PagedParams& p, void* workspace, cudaStream_t stream);
+cudaError_t tc_workspace(const PagedParams& p, size_t* bytes);
 
 inline cudaError_t sm_count(int* n) {
   int dev = 0;
