@@ -84,10 +84,12 @@ cudaError_t launch_join(const PagedParams& p, int bf16, const Scratch& s, int G,
 }  // namespace paged
 
 cudaError_t paged_workspace_bytes(const PagedParams& p, int bf16, size_t* bytes) {
-  return bf16 ? paged::tc_workspace(p, bytes) : paged::simt_workspace(p, bf16, bytes);
+  if (!bf16) return paged::simt_workspace(p, bf16, bytes);
+  return paged::split_supported(p) ? paged::split_workspace(p, bytes) : paged::tc_workspace(p, bytes);
 }
 cudaError_t launch_paged_attn(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream) {
-  return bf16 ? paged::launch_tc(p, workspace, stream) : paged::launch_simt(p, bf16, workspace, stream);
+  if (!bf16) return paged::launch_simt(p, bf16, workspace, stream);
+  return paged::split_supported(p) ? paged::launch_split(p, workspace, stream) : paged::launch_tc(p, workspace, stream);
 }
 
 }  // namespace gdn
