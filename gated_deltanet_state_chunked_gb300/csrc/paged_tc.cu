@@ -12,9 +12,13 @@
 // 2.4e-3; the sum of weights and lse take the unrounded ones.
 //
 // Warps: 0-3 and 4-7 the rows of the two halves, a thread a row: maximum, exponentials, P, and at the end O out; 8-11 load
-// Q, K and V (cp.async: pages of any size and stride, keys behind a request's end as zeros, which a tensor copy
-// could not do); 12 issues the MMAs.  Keys and values pass through a ring of five 32 KB stages.  Registers are moved from the
-// loading and issuing warps to the rows'.  Every hand-off is an mbarrier; every wait is bounded.
+// Q, K and V, 32 rows of a tile each; 12 issues the MMAs.  Keys and values pass through a ring of five 32 KB stages.
+// Units inside a request come by tensor copies, a page (up to 32 rows of it) at a time; the first and last
+// unit of a request, pages of fewer than 8 tokens and strides that a tensor map does not take by cp.async, which fills
+// the places of keys that nobody sees with zeros (what lies there may be no number).  With cp.async alone the loading
+// warps bound the kernel (1,700 clocks to issue a stage: chunk of 2048 at 32K 1,173 us).
+// Registers are moved from the loading and issuing warps to the rows'.  Every hand-off is an mbarrier; every wait
+// is bounded.
 #include <atomic>
 
 #include "paged_work.cuh"
@@ -28,7 +32,7 @@ using namespace tc;
 using tcp::kWaitNs;
 
 constexpr int NT = 512, BM = 256, BN = 128, kStages = 5, kLag = 3;
-constexpr int kRegsLaunch = 128, kRegsRows = 192, kRegsLoad = 72, kRegsIssue = 56;
+constexpr int kRegsLaunch = 128, kRegsRows = 184, kRegsLoad = 80, kRegsIssue = 64;
 static_assert(2 * kRegsRows + kRegsLoad + kRegsIssue <= 4 * kRegsLaunch, "what a launch holds");
 // A stage that is waited for may be kLag loads away from the one being issued, and the issuing warp holds a stage of
 // values until it has multiplied the next keys.
@@ -38,7 +42,7 @@ constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBarAt = kRing + kStages * kTile, 
                    kSmem = kPlanAt + sizeof(PlanSmem);
 static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t cS = 0, cO = 256;  // TMEM columns of the halves' S (and P) and O, 128 each
-constexpr uint64_t kLongNs = 8 * kWaitNs;  // waits that rows computed again may hold up
+constexpr uint64_t kLongNs = 2 * kWaitNs;  // waits that rows computed again may hold up
 
 enum Bar { kFull = 0, kEmpty = kFull + kStages, kQFull = kEmpty + kStages, kQEmpty, kS, kP = kS + 2, kO = kP + 2, kOFree = kO + 2,
            kDrain = kOFree + 2, kBars };
@@ -99,7 +103,24 @@ __device__ __forceinline__ bool second_half(const PagedParams& p, const Request&
   return min(tile_tokens, r.len - tile * tile_tokens) * p.group > 128;
 }
 
-__global__ void __launch_bounds__(NT, 1) paged_tc_kernel(const PagedParams p, const Scratch s, const int tile_tokens) {
+// A tensor map of the key or value pages: d, then tokens, heads and pages by ascending stride, at these places.
+struct PageMap {
+  int token, head, page;  // 1 to 3
+  int rows;               // tokens of a box; 0: no map
+};
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, const PageMap& m, uint64_t* bar, int x, int token,
+                                              int head, int page) {
+  const int c1 = m.token == 1 ? token : m.head == 1 ? head : page, c2 = m.token == 2 ? token : m.head == 2 ? head : page,
+            c3 = m.token == 3 ? token : m.head == 3 ? head : page;
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__global__ void __launch_bounds__(NT, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PageMap mk,
+                    const PageMap mv, const PagedParams p, const Scratch s, const int tile_tokens) {
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + kBarAt);
   volatile int* dead = reinterpret_cast<int*>(sm + kMisc);
@@ -371,28 +392,66 @@ __global__ void __launch_bounds__(NT, 1) paged_tc_kernel(const PagedParams p, co
         const int j = first + u * BN + 32 * quad + lane;
         return u < n && j >= span.lo && j < span.hi ? page_of(p, w.req, j) : -1;
       };
+      // A stage by tensor copies: each warp's 32 rows are a part of one page, or several whole ones.
+      const int atoms = p.d > 64 ? 2 : 1;
+      auto copy_rows = [&](const CUtensorMap* map, const PageMap& m, int st, int j, int page) {
+        const int boxes = 32 / m.rows;
+        if (lane == 0) mbar_arrive_expect_tx(&bar[kFull + st], 32u * 128u * atoms);
+        __syncwarp();
+        if (lane < boxes * atoms) {
+          const int box = lane & (boxes - 1), atom = lane / boxes;
+          tma_load_page(base + kRing + st * kTile + atom * kAtom + (32 * quad + box * m.rows) * 128, map, m, &bar[kFull + st], 64 * atom,
+                        (j + box * m.rows) & mask, w.head, page);
+        }
+        __syncwarp();
+      };
+      auto next_stage = [&](int& st) {
+        st = issued % kStages;
+        return issued < kStages || (ok = wait(kEmpty + st, issued / kStages - 1, kLongNs));
+      };
+      const bool maps = mk.rows > 0 && mv.rows > 0;
       int page = page_at(0);
       for (int u = 0; u < n; ++u) {
-        const int64_t token = (first + u * BN + 32 * quad + lane) & mask;
-        const int64_t k_off = page < 0 ? -1 : page * p.k_page + token * p.k_token;
-        const int64_t v_off = page < 0 ? -1 : page * p.v_page + token * p.v_token;
-        int st = issued % kStages;
-        if (issued >= kStages && !(ok = wait(kEmpty + st, issued / kStages - 1, kLongNs))) break;
-        load_rows(base + kRing + st * kTile, kp, k_off);
-        push(kFull + st);
-        ++issued;
-        page = page_at(u + 1);
-        st = issued % kStages;
-        if (issued >= kStages && !(ok = wait(kEmpty + st, issued / kStages - 1, kLongNs))) break;
-        load_rows(base + kRing + st * kTile, vp, v_off);
-        push(kFull + st);
-        ++issued;
+        const int j0 = first + u * BN, j = j0 + 32 * quad;
+        int st;
+        if (maps && j0 >= span.lo && j0 + BN <= span.hi) {
+          // (the box's page, from the lane of its first key; a page outside the cache reads as zeros)
+          int kb = __shfl_sync(0xffffffffu, page, (lane & (32 / mk.rows - 1)) * mk.rows);
+          int vb = __shfl_sync(0xffffffffu, page, (lane & (32 / mv.rows - 1)) * mv.rows);
+          kb = kb < 0 ? p.n_pages : kb;
+          vb = vb < 0 ? p.n_pages : vb;
+          if (!next_stage(st)) break;
+          copy_rows(&map_k, mk, st, j, kb);
+          ++issued;
+          page = page_at(u + 1);
+          if (!next_stage(st)) break;
+          copy_rows(&map_v, mv, st, j, vb);
+          ++issued;
+          if (u == 0) flush();  // (the queries, which nothing else pushes on)
+        } else {
+          const int64_t token = (j + lane) & mask;
+          const int64_t k_off = page < 0 ? -1 : page * p.k_page + token * p.k_token;
+          const int64_t v_off = page < 0 ? -1 : page * p.v_page + token * p.v_token;
+          if (!next_stage(st)) break;
+          load_rows(base + kRing + st * kTile, kp, k_off);
+          push(kFull + st);
+          ++issued;
+          page = page_at(u + 1);
+          if (!next_stage(st)) break;
+          load_rows(base + kRing + st * kTile, vp, v_off);
+          push(kFull + st);
+          ++issued;
+          if (maps) flush();  // (nothing pushes these on while tensor copies follow)
+        }
       }
       if (!ok) break;
       ++items;
       w.advance(p, tile_tokens, n);
     }
     flush();
+    if (!ok)  // let this warp's tensor copies in flight land (their stages may lack other warps' arrivals: briefly)
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        mbar_wait(&bar[kFull + i % kStages], (uint32_t)((i / kStages) & 1), kWaitNs / 100);
   } else {
     regs_dec<kRegsIssue>();
     if (quad == 0) {
@@ -404,10 +463,12 @@ __global__ void __launch_bounds__(NT, 1) paged_tc_kernel(const PagedParams p, co
       auto qk = [&](int half, int st) {
         if (elect_one()) {
           const uint64_t q = dQ + (uint64_t)((half * kTile) >> 4), k = dK + (uint64_t)((st * kTile) >> 4);
-          for (int i = 0; i < nk; ++i) {
-            const uint64_t off = (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4);
-            mma_bf16(tmem + cS + 128 * half, q + off, k + off, idQK, i > 0);
-          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < nk) {
+              const uint64_t off = (uint64_t)(((i >> 2) * kAtom + (i & 3) * 32) >> 4);
+              mma_bf16(tmem + cS + 128 * half, q + off, k + off, idQK, i > 0);
+            }
           mma_commit(&bar[kS + half]);
         }
         __syncwarp();
@@ -488,6 +549,39 @@ cudaError_t check_registers() {
   return cudaSuccess;
 }
 
+// The map of pages with these strides; its `rows` stay 0 where there is none.
+void make_page_map(CUtensorMap* map, PageMap* m, const PagedParams& p, const void* base, int64_t page, int64_t token, int64_t head) {
+  *m = PageMap{1, 2, 3, 0};
+  auto enc = encode_fn();
+  const int size = 1 << p.page_shift, rows = size < 32 ? size : 32;
+  if (!enc || rows < 8) return;  // (a box starts at a multiple of 8 rows of the swizzled tile)
+  struct Dim {
+    int64_t stride;
+    int64_t size;
+    int box;
+    int* at;
+  } dims[3] = {{token, size, rows, &m->token}, {head, p.h_kv, 1, &m->head}, {page, p.n_pages, 1, &m->page}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j + 1 < 3; ++j)
+      if (dims[j].stride > dims[j + 1].stride) {
+        const Dim x = dims[j];
+        dims[j] = dims[j + 1];
+        dims[j + 1] = x;
+      }
+  cuuint64_t sizes[4] = {(cuuint64_t)p.d, 0, 0, 0}, strides[3];
+  cuuint32_t box[4] = {64, 0, 0, 0}, es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    if (dims[i].stride == 0 && dims[i].size > 1) return;
+    *dims[i].at = i + 1;
+    sizes[i + 1] = (cuuint64_t)dims[i].size;
+    strides[i] = (cuuint64_t)(dims[i].stride > 0 ? dims[i].stride * 2 : 16);
+    box[i + 1] = (cuuint32_t)dims[i].box;
+  }
+  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), sizes, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+    m->rows = rows;
+}
+
 }  // namespace
 
 cudaError_t tc_workspace(const PagedParams& p, size_t* bytes) {
@@ -506,7 +600,11 @@ cudaError_t launch_tc(const PagedParams& p, void* workspace, cudaStream_t stream
   if (e != cudaSuccess) return e;
   const int tile_tokens = BM / p.group;
   const Scratch s = scratch_at(workspace, sms, BM, p.d);
-  paged_tc_kernel<<<sms, NT, kSmem, stream>>>(p, s, tile_tokens);
+  CUtensorMap map_k{}, map_v{};
+  PageMap mk, mv;
+  make_page_map(&map_k, &mk, p, p.k, p.k_page, p.k_token, p.k_head);
+  make_page_map(&map_v, &mv, p, p.v, p.v_page, p.v_token, p.v_head);
+  paged_tc_kernel<<<sms, NT, kSmem, stream>>>(map_k, map_v, mk, mv, p, s, tile_tokens);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_join(p, 1, s, sms, BM, tile_tokens, stream);
 }
