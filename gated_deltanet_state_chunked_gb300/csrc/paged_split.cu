@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(NT, 2) paged_split_kernel(const PagedParams p,
       for (int i = 0; i < 2; ++i) {
         const Row x = row_of(p, rq, w.head, w.tile, tile_tokens, 16 * t + 8 * i + lane / 4);
         const int pos = rq.kv - rq.len + x.t;
-        hi[t][i] = x.live ? pos + 1 : 0;
-        lo[t][i] = p.window ? max(0, pos - p.window + 1) : 0;
+        // (a row that is none sees everything, so that it calls for no masking; nothing of it is stored)
+        hi[t][i] = x.live ? pos + 1 : INT_MAX;
+        lo[t][i] = x.live && p.window ? max(0, pos - p.window + 1) : 0;
         ref[t][i] = -CUDART_INF_F;
         l[t][i] = 0.f;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(rq.q0 + x.t) * p.q_stride + (int64_t)x.h * p.d;
@@ -374,7 +375,7 @@ int rows_of(const PagedParams& p) { return (long long)p.max_q * p.group <= 16 ? 
 
 }  // namespace
 
-bool split_supported(const PagedParams& p) { return (long long)p.max_q * p.group <= 16; }
+bool split_supported(const PagedParams& p) { return (long long)p.max_q * p.group <= 32; }
 
 cudaError_t split_workspace(const PagedParams& p, size_t* bytes) {
   int sms = 0;

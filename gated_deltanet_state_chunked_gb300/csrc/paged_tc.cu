@@ -98,6 +98,24 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Four lanes with a row of four 16-byte pieces each: afterwards lane i has piece i of the four rows in turn, so that
+// a store of the four writes 64 bytes of one row (a thread's own row would go out in 16-byte pieces of 32 lines).
+__device__ __forceinline__ void swap_pieces(uint32_t (&y)[16], int lane) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & o)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // piece i + o of the lower lane against piece i of the upper one
+          const bool upper = lane & o;
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? y[4 * i + e] : y[4 * (i + o) + e], o);
+          if (upper) y[4 * i + e] = got;
+          else y[4 * (i + o) + e] = got;
+        }
+      }
+}
+
 // Rows of a tile's second half: none for short windows.
 __device__ __forceinline__ bool second_half(const PagedParams& p, const Request& r, int tile, int tile_tokens) {
   return min(tile_tokens, r.len - tile * tile_tokens) * p.group > 128;
@@ -188,7 +206,8 @@ __global__ void __launch_bounds__(NT, 1)
         const int first = (w.span.lo / BN + w.at) * BN;
         const Row x = row_of(p, rq, w.head, w.tile, tile_tokens, r);
         const int pos = rq.kv - rq.len + x.t;
-        const int hi = x.live ? pos + 1 : 0, lo = p.window ? max(0, pos - p.window + 1) : 0;
+        // (a row that is none sees everything, so that it calls for no masking; nothing of it is stored)
+        const int hi = x.live ? pos + 1 : INT_MAX, lo = x.live && p.window ? max(0, pos - p.window + 1) : 0;
         float ref = -CUDART_INF_F, l = 0.f;
         for (int u = 0; u < n; ++u, ++done) {
           if (!(ok = wait(kS + group, done))) break;
@@ -279,6 +298,15 @@ __global__ void __launch_bounds__(NT, 1)
         const float f = row_factor(l, sees);
         const size_t slot_row = (size_t)(w.at ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * BM + r;
         const size_t out = (size_t)(rq.q0 + x.t) * p.h_q + x.h;
+        unsigned char* const mine = !x.live ? nullptr
+                                    : whole ? reinterpret_cast<unsigned char*>(static_cast<__nv_bfloat16*>(p.O) + out * p.d)
+                                            : reinterpret_cast<unsigned char*>(s.rows + slot_row * p.d);
+        unsigned char* to[4];  // the rows of this lane's four
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          to[j] = reinterpret_cast<unsigned char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), (lane & ~3) + j));
+          if (to[j]) to[j] += 16 * (lane & 3);
+        }
         bool fine = true;
 #pragma unroll 1
         for (int c = 0; c < p.d; c += 32) {
@@ -290,20 +318,27 @@ __global__ void __launch_bounds__(NT, 1)
             o[j] = sees ? o[j] * f : 0.f;
             fine = fine && (c + j >= p.d || fabsf(o[j]) <= 3.402823466e38f);
           }
-          if (x.live) {
+          if (whole) {
+            uint32_t y[16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              if (c + j < p.d) {
-                if (whole) {
-                  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + out * p.d + c + j) =
-                      make_uint4(pack_bf16(o[j], o[j + 1]), pack_bf16(o[j + 2], o[j + 3]), pack_bf16(o[j + 4], o[j + 5]),
-                                 pack_bf16(o[j + 6], o[j + 7]));
-                } else {
-                  float4* to = reinterpret_cast<float4*>(s.rows + slot_row * p.d + c + j);
-                  to[0] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                  to[1] = make_float4(o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
-                }
-              }
+            for (int j = 0; j < 16; ++j) y[j] = pack_bf16(o[2 * j], o[2 * j + 1]);
+            swap_pieces(y, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (to[j] && c + 8 * (lane & 3) < p.d)
+                *reinterpret_cast<uint4*>(to[j] + 2 * c) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t y[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(o[16 * half + j]);
+              swap_pieces(y, lane);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (to[j] && c + 16 * half + 4 * (lane & 3) < p.d)
+                  *reinterpret_cast<uint4*>(to[j] + 4 * (c + 16 * half)) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+            }
           }
         }
         tc_fence_before();
