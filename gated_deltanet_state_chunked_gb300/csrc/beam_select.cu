@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kRowNT, 2) beam_rows_kernel(BeamParams p, Beam
 
 // A request's candidates are its beams' slices' lists: candidate i is entry i % best of list i / best, a beam's lists side
 // by side.  Of equal totals the lower beam stands first, and within a beam the larger key.
-__global__ void __launch_bounds__(kMergeNT) beam_merge_kernel(BeamParams p, BeamWork w) {
+__global__ void __launch_bounds__(kMergeNT, 3) beam_merge_kernel(BeamParams p, BeamWork w) {
   constexpr int kGroups = kMergeNT / 4, kWarps = kMergeNT / 32;
   __shared__ double base[kMaxBeams];
   __shared__ uint64_t group[kGroups], bound, total[kMostCandidates], w_total[kWarps];

@@ -8,7 +8,7 @@ namespace {
 // o = sum_c (w_c / sum w) o_c, w_c = l_c 2^(m_c - max m): one warp a row, its pieces in the order of the
 // keys.  The statistics are read side by side, then the rows eight at a time: two trips to L2 for most items.
 template <typename T>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p, Scratch s, int BM, int tile_tokens) {
+__global__ void __launch_bounds__(256, 3) paged_join_kernel(PagedParams p, Scratch s, int BM, int tile_tokens) {
   tc::grid_dep_wait();
   const Shared sh = s.shared[blockIdx.x];
   if (sh.req < 0) return;
@@ -39,16 +39,21 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p, Scratch 
       const float2 st = s.stat[slot(k0 + lane)];
       w_mine = st.y * exp2f(st.x - ref) * f;
     }
-    const int most = min(32, n - k0);
-#pragma unroll 8
-    for (int k = 0; k < most; ++k) {
-      const float w = __shfl_sync(0xffffffffu, w_mine, k);
-      if (lane < d4) {
-        const float4 v = reinterpret_cast<const float4*>(s.rows + slot(k0 + k) * p.d)[lane];
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+    // (eight rows under way at a time)
+    constexpr int kAhead = 8;
+    for (int k = 0; k < min(32, n - k0); k += kAhead) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        v[i] = lane < d4 && k0 + k + i < n ? reinterpret_cast<const float4*>(s.rows + slot(k0 + k + i) * p.d)[lane]
+                                           : float4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float w = __shfl_sync(0xffffffffu, w_mine, k + i);
+        acc.x = fmaf(w, v[i].x, acc.x);
+        acc.y = fmaf(w, v[i].y, acc.y);
+        acc.z = fmaf(w, v[i].z, acc.z);
+        acc.w = fmaf(w, v[i].w, acc.w);
       }
     }
   }

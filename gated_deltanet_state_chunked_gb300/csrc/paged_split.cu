@@ -375,7 +375,7 @@ int rows_of(const PagedParams& p) { return (long long)p.max_q * p.group <= 16 ? 
 
 }  // namespace
 
-bool split_supported(const PagedParams& p) { return (long long)p.max_q * p.group <= 32; }
+bool split_supported(const PagedParams& p) { return (long long)p.max_q * p.group <= 16; }
 
 cudaError_t split_workspace(const PagedParams& p, size_t* bytes) {
   int sms = 0;

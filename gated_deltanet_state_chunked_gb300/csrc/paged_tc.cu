@@ -98,24 +98,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Four lanes with a row of four 16-byte pieces each: afterwards lane i has piece i of the four rows in turn, so that
-// a store of the four writes 64 bytes of one row (a thread's own row would go out in 16-byte pieces of 32 lines).
-__device__ __forceinline__ void swap_pieces(uint32_t (&y)[16], int lane) {
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!(i & o)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // piece i + o of the lower lane against piece i of the upper one
-          const bool upper = lane & o;
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? y[4 * i + e] : y[4 * (i + o) + e], o);
-          if (upper) y[4 * i + e] = got;
-          else y[4 * (i + o) + e] = got;
-        }
-      }
-}
-
 // Rows of a tile's second half: none for short windows.
 __device__ __forceinline__ bool second_half(const PagedParams& p, const Request& r, int tile, int tile_tokens) {
   return min(tile_tokens, r.len - tile * tile_tokens) * p.group > 128;
@@ -219,12 +201,12 @@ __global__ void __launch_bounds__(NT, 1)
           const int j0 = first + u * BN;
           if (__any_sync(0xffffffffu, lo > j0 || hi < j0 + BN)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {  // bits lo - j .. hi - j - 1 of the 32 columns
+              const int from = max(0, lo - j0 - 32 * i), to = min(32, max(0, hi - j0 - 32 * i));
+              const uint32_t seen = from >= to ? 0u : (0xffffffffu << from) & (0xffffffffu >> (32 - to));
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const int key = j0 + 32 * i + j;
-                a[i][j] = key >= lo && key < hi ? a[i][j] : masked;
-              }
+              for (int j = 0; j < 32; ++j) a[i][j] = (seen >> j) & 1u ? a[i][j] : masked;
+            }
           }
           float top[4];
           if (s2 > 0.f) {
@@ -298,47 +280,33 @@ __global__ void __launch_bounds__(NT, 1)
         const float f = row_factor(l, sees);
         const size_t slot_row = (size_t)(w.at ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * BM + r;
         const size_t out = (size_t)(rq.q0 + x.t) * p.h_q + x.h;
-        unsigned char* const mine = !x.live ? nullptr
-                                    : whole ? reinterpret_cast<unsigned char*>(static_cast<__nv_bfloat16*>(p.O) + out * p.d)
-                                            : reinterpret_cast<unsigned char*>(s.rows + slot_row * p.d);
-        unsigned char* to[4];  // the rows of this lane's four
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          to[j] = reinterpret_cast<unsigned char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), (lane & ~3) + j));
-          if (to[j]) to[j] += 16 * (lane & 3);
-        }
         bool fine = true;
+        // (16 columns at a time: an item's end runs through this code once, and what it costs is fetching the code.  Wider
+        // steps that store 64 bytes of a row at once: 10,000 clocks of an item, 38,000 the first time)
 #pragma unroll 1
-        for (int c = 0; c < p.d; c += 32) {
-          float o[32];
-          tmem_ld32(at_o + c, o);
+        for (int c = 0; c < p.d; c += 16) {
+          float o[16];
+          tmem_ld16(at_o + c, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < 16; ++j) {
             o[j] = sees ? o[j] * f : 0.f;
-            fine = fine && (c + j >= p.d || fabsf(o[j]) <= 3.402823466e38f);
+            fine = fine && fabsf(o[j]) <= 3.402823466e38f;  // (columns behind d are zeros times weights, or like the others)
           }
-          if (whole) {
-            uint32_t y[16];
+          if (x.live) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = pack_bf16(o[2 * j], o[2 * j + 1]);
-            swap_pieces(y, lane);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (to[j] && c + 8 * (lane & 3) < p.d)
-                *reinterpret_cast<uint4*>(to[j] + 2 * c) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-          } else {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t y[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(o[16 * half + j]);
-              swap_pieces(y, lane);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (to[j] && c + 16 * half + 4 * (lane & 3) < p.d)
-                  *reinterpret_cast<uint4*>(to[j] + 4 * (c + 16 * half)) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-            }
+            for (int j = 0; j < 16; j += 8)
+              if (c + j < p.d) {
+                if (whole) {
+                  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + out * p.d + c + j) =
+                      make_uint4(pack_bf16(o[j], o[j + 1]), pack_bf16(o[j + 2], o[j + 3]), pack_bf16(o[j + 4], o[j + 5]),
+                                 pack_bf16(o[j + 6], o[j + 7]));
+                } else {
+                  float4* to = reinterpret_cast<float4*>(s.rows + slot_row * p.d + c + j);
+                  to[0] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                  to[1] = make_float4(o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
+                }
+              }
           }
         }
         tc_fence_before();
