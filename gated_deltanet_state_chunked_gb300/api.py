@@ -181,6 +181,7 @@ def gdn_compose(T_list, Slocal_list, S_in=None, *, S_out=None, stream=None):
 # on the current device and stream, pointers as plain integers.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _want(name, t, device, dtype, shape):
@@ -216,7 +217,7 @@ def _launch(call, where, ref, stream, outputs, *args):
         if stream != torch.cuda.current_stream(device) or torch.cuda.current_device() != device:
             with torch.cuda.stream(stream):
                 return _launch(call, where, ref, None, outputs, *args)
-    elif torch.cuda.current_device() != device:
+    elif _current_device() != device:
         with torch.cuda.device(device):
             return _launch(call, where, ref, None, outputs, *args)
     made = [torch.empty(t[0], dtype=t[1], device=ref.device) if type(t) is tuple else t for t in outputs]
@@ -350,66 +351,69 @@ def gdn_verify_draft(target, drafted, uniforms, draft=None, draft_lens=None, *, 
     return counts, tokens
 
 
+def _placed(name, t, device, dtype, shape):
+    """Raise for what _want refuses, strides apart."""
+    _need_cuda(name, t[:0], dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{device}")
+
+
 def _token_rows(name, t, device, dtype, shape):
     """(data_ptr, elements between tokens) of t [T, h, d]: a token's heads lie one after another, the
     tokens may be apart (a slice of a projection's rows)."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _need_cuda(name, t[:0], dtype)
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{device}")
+        _placed(name, t, device, dtype, shape)
     T, h, d = shape
-    if t.is_contiguous():
-        return t.data_ptr(), h * d
     step, head, one = t.stride()
-    if one != 1 and d > 1 or head != d and h > 1:
+    if (one != 1 and d > 1 or head != d and h > 1) and t.numel():
         raise ValueError(f"{name}: a token's heads must lie one after another")
-    return t.data_ptr(), h * d if T == 1 else step
+    return t.data_ptr(), step if T > 1 else h * d
 
 
 def _page_strides(name, t, device, dtype, shape):
     """Elements between the pages, tokens and heads of t [n_pages, page_size, h_kv, d] (0 where there is one)."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _need_cuda(name, t[:0], dtype)
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{device}")
-    s = t.stride()
-    if s[3] != 1 and shape[3] > 1:
+        _placed(name, t, device, dtype, shape)
+    page, token, head, one = t.stride()
+    if one != 1 and shape[3] > 1:
         raise ValueError(f"{name}: the values of a head must lie one after another")
-    return [step if size > 1 else 0 for step, size in zip(s[:3], shape)]
+    return page if shape[0] > 1 else 0, token if shape[1] > 1 else 0, head if shape[2] > 1 else 0
 
 
-def _paged(T, h_q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_q):
+def _paged(T, h_q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_q, d, window=0, scale=0.0):
     """The parts that gdn_kv_append and gdn_paged_attn share: GdnPagedDims without the tokens' strides, and the
     pointers of page_table, kv_lens and cu_seqlens."""
     dt = k_pages.dtype
-    if dt not in _DTYPE:
+    code = _DTYPE.get(dt)
+    if code is None:
         raise ValueError(f"unsupported dtype {dt}")
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be [n_pages, page_size, h_kv, d]")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n, table_width]")
     shape = k_pages.shape
-    n_pages, page, h_kv, d = shape
+    n_pages, page, h_kv, d_pages = shape
+    if d_pages != d:
+        raise ValueError(f"heads of {d} values, the pages have heads of {d_pages}")
     n, width = page_table.shape
     if n == 0 and T:
         raise ValueError(f"{T} tokens of no requests")
     if max_q is None:
         max_q = T if cu_seqlens is not None else T // n if n else 0
-    _fits(n, T, max_q, h_q, h_kv, d, page, n_pages, width)
+    _fits(n, T, max_q, h_q, h_kv, d, page, n_pages, width, window)
     dev = _cuda_index("k_pages", k_pages)
-    ks, vs = _page_strides("k_pages", k_pages, dev, dt, shape), _page_strides("v_pages", v_pages, dev, dt, shape)
-    if page_table.is_contiguous():
-        table, step = _want("page_table", page_table, dev, torch.int32, (n, width)), width
-    else:  # rows of a wider table
-        if page_table.stride(1) != 1 and width > 1:
-            raise ValueError("page_table: a request's pages must lie one after another")
-        _want("page_table", page_table[:0], dev, torch.int32, (0, width))
-        table, step = page_table.data_ptr(), page_table.stride(0) if n > 1 else width
-    dims = _lib.GdnPagedDims(n, T, max(max_q, 1), h_q, h_kv, d, page, n_pages, width, _DTYPE[dt], 0, 0.0, step, 0, 0, 0, *ks, *vs)
-    return dims, (table, _want("kv_lens", kv_lens, dev, torch.int32, (n,)),
-                  _want("cu_seqlens", cu_seqlens, dev, torch.int32, (n + 1,))), dev, dt
+    i32 = torch.int32
+    if page_table.dtype is not i32 or page_table.get_device() != dev:
+        _placed("page_table", page_table, dev, i32, (n, width))
+    step, one = page_table.stride()  # (rows of a wider table will do)
+    if one != 1 and width > 1:
+        raise ValueError("page_table: a request's pages must lie one after another")
+    dims = _lib.GdnPagedDims(n, T, max_q or 1, h_q, h_kv, d, page, n_pages, width, code, window, scale,
+                             step if n > 1 else width, 0, 0, 0, *_page_strides("k_pages", k_pages, dev, dt, shape),
+                             *_page_strides("v_pages", v_pages, dev, dt, shape))
+    return dims, page_table.data_ptr(), _want("kv_lens", kv_lens, dev, i32, (n,)), \
+        _want("cu_seqlens", cu_seqlens, dev, i32, (n + 1,)), dev, dt
 
 
 def gdn_kv_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, q=None, q_out=None, inv_freq=None,
@@ -418,18 +422,18 @@ def gdn_kv_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, 
 
     k, v: [T, h_kv, d], bf16 or fp32, tokens packed request after request (a slice of wider rows will do);
     k_pages, v_pages: [n_pages, page_size, h_kv, d] of the same dtype, any strides (of multiples of 16 bytes) with the
-    values of a head together, written in place; page_table: int32 [n, width]; kv_lens: int32 [n] on the device, the tokens in the
-    cache with the new ones (negative: padding); cu_seqlens: int32 [n + 1] on the device, or None: T / n new tokens
-    each.  inv_freq: fp32 [rotary_dim / 2] or None (no rotation); positions: int32 [T] or [axes, T], or None (the place in the
-    cache); sections: pairs that turn by each axis; neighbours: pairs are values 2i and 2i + 1 instead of i and
-    i + rotary_dim / 2; max_q: the most new tokens of a request, where it is known.
+    values of a head together, written in place; page_table: int32 [n, width]; kv_lens: int32 [n] on the device, the
+    tokens in the cache with the new ones (negative: padding); cu_seqlens: int32 [n + 1] on the device, or None: T / n
+    new tokens each.  inv_freq: fp32 [rotary_dim / 2] or None (no rotation); positions: int32 [T] or [axes, T], or None
+    (the place in the cache); sections: pairs that turn by each axis; neighbours: pairs are values 2i and 2i + 1 instead
+    of i and i + rotary_dim / 2; max_q: the most new tokens of a request, where it is known.
     Returns the rotated queries [T, h_q, d], None without q."""
     lib = _lib.load()
     T, h_kv, d = k.shape
     h_q = h_kv if q is None else q.shape[1]
-    dims, tables, dev, dt = _paged(T, h_q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_q)
-    if k_pages.shape[2:] != k.shape[1:]:
-        raise ValueError(f"k has heads {tuple(k.shape[1:])}, the pages {tuple(k_pages.shape[2:])}")
+    dims, table, lens, cu, dev, dt = _paged(T, h_q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_q, d)
+    if k_pages.shape[2] != h_kv:
+        raise ValueError(f"k has {h_kv} heads, the pages {k_pages.shape[2]}")
     k_ptr, dims.k_stride = _token_rows("k", k, dev, dt, (T, h_kv, d))
     v_ptr, dims.v_stride = _token_rows("v", v, dev, dt, (T, h_kv, d))
     q_ptr, rotary, freq_ptr, pos_ptr = None, None, None, None
@@ -440,21 +444,22 @@ def gdn_kv_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, 
         raise ValueError("q_out without q")
     if inv_freq is not None:
         axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
-        sections = (0,) if sections is None else tuple(sections)
-        if axes > 1 and len(sections) != axes:
-            raise ValueError(f"{axes} axes of positions, {len(sections)} sections")
+        if axes > 1 and (sections is None or len(sections) != axes):
+            raise ValueError(f"{axes} axes of positions, sections {sections}")
         if axes > _lib.GDN_MAX_AXES:
             raise ValueError(f"at most {_lib.GDN_MAX_AXES} axes of positions, got {axes}")
         freq_ptr = _want("inv_freq", inv_freq, dev, torch.float32, (inv_freq.shape[0],))
         if positions is not None:
             pos_ptr = _want("positions", positions, dev, torch.int32, (T,) if positions.dim() == 1 else (axes, T))
-        rotary = _lib.GdnRotary(2 * inv_freq.shape[0], 1 if neighbours else 0, axes,
-                                (ctypes.c_int32 * _lib.GDN_MAX_AXES)(*(sections if axes > 1 else ())))
+        rotary = _lib.GdnRotary(2 * inv_freq.shape[0], 1 if neighbours else 0, axes)
+        if axes > 1:
+            _fits(*sections)
+            rotary.sections[:axes] = sections
     elif positions is not None or sections is not None:
         raise ValueError("positions and sections need inv_freq")
     return _launch(lib.gdn_kv_append, "gdn_kv_append", k_pages, stream,
-                   (None if q is None else ((T, h_q, d), dt) if q_out is None else q_out,), dims, rotary, q_ptr, k_ptr, v_ptr,
-                   freq_ptr, pos_ptr, *tables, k_pages.data_ptr(), v_pages.data_ptr())[0]
+                   (None if q is None else ((T, h_q, d), dt) if q_out is None else q_out,), dims, rotary, q_ptr, k_ptr,
+                   v_ptr, freq_ptr, pos_ptr, table, lens, cu, k_pages.data_ptr(), v_pages.data_ptr())[0]
 
 
 def gdn_paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, max_q=None, scale=None, window=0,
@@ -469,18 +474,14 @@ def gdn_paged_attn(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *,
     and outside every range are left as they were (undefined when O is allocated here)."""
     lib = _lib.load()
     T, h_q, d = q.shape
-    dims, tables, dev, dt = _paged(T, h_q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_q)
-    if k_pages.shape[3] != d:
-        raise ValueError(f"q has heads of {d} values, the pages of {k_pages.shape[3]}")
-    _fits(window)
+    dims, table, lens, cu, dev, dt = _paged(T, h_q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, max_q, d, window,
+                                            d ** -0.5 if scale is None else scale)
     q_ptr, dims.q_stride = _token_rows("q", q, dev, dt, (T, h_q, d))
-    dims.window = window
-    dims.scale = d ** -0.5 if scale is None else scale
     _want("O_out", O_out, dev, dt, (T, h_q, d))
     _want("lse_out", lse_out, dev, torch.float32, (T, h_q))
     return _launch(lib.gdn_paged_attn, "gdn_paged_attn", q, stream,
                    (((T, h_q, d), dt) if O_out is None else O_out, lse_out), dims, q_ptr, k_pages.data_ptr(),
-                   v_pages.data_ptr(), *tables)[0]
+                   v_pages.data_ptr(), table, lens, cu)[0]
 
 
 def gdn_beam_select(logits, scores, best=None, *, scores_out=None, parents_out=None, tokens_out=None, stream=None):

@@ -76,75 +76,137 @@ __device__ __forceinline__ U bound_of(const U* group, U* result, int best) {
   return *result;
 }
 
-// PER values a thread, in slices of up to 512 PER.  Bound by HBM where there are many rows: 15 instructions a value beside
-// its load; for few rows by the chain of loads, maximum, bound and ranks of one slice.
-template <typename T, int PER>
-__global__ void __launch_bounds__(kRowNT, 2) beam_rows_kernel(BeamParams p, BeamWork w) {
-  constexpr int kGroups = kRowNT / 4, kWarps = kRowNT / 32;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two fp32 operations in one instruction (values as register pairs).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Place in the slice of a thread's i-th value: one value, or two neighbours, to a load.
+template <int VEC>
+__device__ __forceinline__ int place_of(int i) {
+  return VEC == 2 ? 2 * (threadIdx.x + (i >> 1) * kRowNT) + (i & 1) : threadIdx.x + i * kRowNT;
+}
+
+// PER values a thread, in slices of up to 512 PER.  Bound by HBM where there are many rows: about 9 instructions a value,
+// and several CTAs an SM so that the loads of one cover the work of the others; for few rows by the chain of load, maximum,
+// bound and ranks of one slice.  VEC 2: bf16 rows that start at even places, two values to a load.
+template <typename T, int PER, int VEC>
+__global__ void __launch_bounds__(kRowNT, 3) beam_rows_kernel(BeamParams p, BeamWork w) {
+  constexpr int kWarps = kRowNT / 32, kGroups = 2 * kMaxBeams;
   __shared__ __align__(16) uint32_t group[kGroups];
   __shared__ uint32_t bound;
   __shared__ uint64_t cand[kMostCandidates], w_best[kWarps];
   __shared__ float w_max[kWarps];
-  __shared__ double w_sum[kWarps];
-  __shared__ int count;
+  __shared__ int w_coarse[kWarps], w_fine[kWarps], count, nan;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / w.slices, slice = blockIdx.x - row * w.slices;
   tc::grid_dep_launch();
-  const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-  const int v0 = slice * w.slice_len, v1 = min(p.vocab, v0 + w.slice_len);
+  const int v0 = slice * w.slice_len, len = min(p.vocab - v0, w.slice_len);
+  const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride + v0;
   float a[PER];
+  if (VEC == 2) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int v = v0 + tid + i * kRowNT;
-    a[i] = v < v1 ? load_f(x + v) : -CUDART_INF_F;
+    for (int i = 0; i < PER; i += 2) {
+      const int v = place_of<VEC>(i);
+      uint32_t u = 0xff80ff80u;  // -inf, -inf
+      if (v + 1 < len) u = __ldg(reinterpret_cast<const unsigned int*>(x + v));
+      else if (v < len) u = 0xff800000u | __ldg(reinterpret_cast<const unsigned short*>(x + v));
+      a[i] = __uint_as_float(u << 16);
+      a[i + 1] = __uint_as_float(u & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) a[i] = place_of<VEC>(i) < len ? load_f(x + place_of<VEC>(i)) : -CUDART_INF_F;
   }
   float top = -CUDART_INF_F;
 #pragma unroll
   for (int i = 0; i < PER; ++i) top = fmaxf(top, a[i]);
   const uint32_t mine = order_of(top);
+  // (up to 32 continuations are bounded by the maxima of 64 groups of 8 threads, more by those of 128 groups of 4)
   uint32_t g = max(mine, shfl_xor(mine, 1));
   g = max(g, shfl_xor(g, 2));
-  if ((lane & 3) == 0) group[tid >> 2] = g;
+  const bool few = p.best <= kMaxBeams / 2;
+  if (few) g = max(g, shfl_xor(g, 4));
+  if ((lane & (few ? 7 : 3)) == 0) group[tid >> (few ? 3 : 2)] = g;
   float m = top;
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, shfl_xor(m, o));
   if (lane == 0) w_max[warp] = m;
-  if (tid == 0) count = 0;
+  if (tid == 0) count = nan = 0;
   __syncthreads();
   m = w_max[0];
 #pragma unroll
   for (int i = 1; i < kWarps; ++i) m = fmaxf(m, w_max[i]);
-  // The sum: each exponential's whole multiples of 2^-16 and what is left of it are added up apart, so that a thread's
-  // additions lose nothing (the multiples' sum is exact), and the threads' sums in fp64.
+  // The sum: each exponential's whole multiples of 2^-16 and what is left of it are added up apart.  A thread's additions
+  // of multiples are exact, and so are the threads' sums as integers (of 2^-16: at most 512 PER 2^16 <= 2^29; of 2^-33).
   {
+    static_assert(PER <= 16, "sums as 32-bit integers");
     const float ref = m == -CUDART_INF_F ? 0.f : m;
-    float coarse = 0.f, fine = 0.f;
+    const uint64_t mm = pair(-ref, -ref), log2e = pair(1.4426950408889634f, 1.4426950408889634f);
+    const uint64_t up = pair(192.f, 192.f), down = pair(-192.f, -192.f);  // (in [2^7, 2^8): steps of 2^-16)
+    const uint64_t minus = pair(-1.f, -1.f);
+    uint64_t coarse = 0ull, fine = 0ull;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const float e = expf(a[i] - ref), c = (e + 192.f) - 192.f;  // (192 lies in [2^7, 2^8): steps of 2^-16)
-      coarse += c;
-      fine += e - c;
+    for (int i = 0; i < PER; i += 2) {
+      float t0, t1;
+      unpair(mul2(add2(pair(a[i], a[i + 1]), mm), log2e), t0, t1);
+      const uint64_t e = pair(exp2_fast(t0), exp2_fast(t1)), c = add2(add2(e, up), down);
+      coarse = add2(coarse, c);
+      fine = add2(fine, add2(e, mul2(c, minus)));
     }
-    double s = (double)coarse + (double)fine;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += shfl_xor(s, o);
-    if (lane == 0) w_sum[warp] = s;
+    float c0, c1, f0, f1;
+    unpair(coarse, c0, c1);
+    unpair(fine, f0, f1);
+    const float c = c0 + c1, f = f0 + f1;
+    const bool bad = c != c;  // (a NaN among the values, or +inf - +inf)
+    if (__any_sync(0xffffffffu, bad) && lane == 0) nan = 1;
+    const int ci = __reduce_add_sync(0xffffffffu, bad ? 0 : (int)(c * 65536.f));
+    const int fi = __reduce_add_sync(0xffffffffu, bad ? 0 : __float2int_rn(f * 8589934592.f));
+    if (lane == 0) {
+      w_coarse[warp] = ci;
+      w_fine[warp] = fi;
+    }
   }
-  const uint32_t least = bound_of<kGroups>(group, &bound, p.best);
+  const uint32_t least = few ? bound_of<kGroups / 2>(group, &bound, p.best) : bound_of<kGroups>(group, &bound, p.best);
   if (tid == 0) {
-    double s = 0.;
-    for (int i = 0; i < kWarps; ++i) s += w_sum[i];
-    w.sum[blockIdx.x] = s;
+    long long c = 0, f = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      c += w_coarse[i];
+      f += w_fine[i];
+    }
+    w.sum[blockIdx.x] = nan ? CUDART_NAN : (double)((c << 17) + f) * 0x1p-33;
     w.max[blockIdx.x] = m;
   }
   if (mine >= least) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int v = v0 + tid + i * kRowNT;
-      const uint64_t k = v < v1 ? key_of(a[i], v) : 0ull;
-      if (k && (uint32_t)(k >> 32) >= least) {
-        const int n = atomicAdd(&count, 1);
-        if (n < kMostCandidates) cand[n] = k;
+      if (order_of(a[i]) >= least) {
+        const int v = place_of<VEC>(i);
+        const uint64_t k = v < len ? key_of(a[i], v0 + v) : 0ull;
+        if (k) {
+          const int n = atomicAdd(&count, 1);
+          if (n < kMostCandidates) cand[n] = k;
+        }
       }
     }
   }
@@ -165,8 +227,8 @@ __global__ void __launch_bounds__(kRowNT, 2) beam_rows_kernel(BeamParams p, Beam
       uint64_t k = 0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int v = v0 + tid + i * kRowNT;
-        const uint64_t c = v < v1 ? key_of(a[i], v) : 0ull;
+        const int v = place_of<VEC>(i);
+        const uint64_t c = v < len ? key_of(a[i], v0 + v) : 0ull;
         if (c < last && c > k) k = c;
       }
 #pragma unroll
@@ -297,13 +359,13 @@ __global__ void __launch_bounds__(kMergeNT, 3) beam_merge_kernel(BeamParams p, B
 }
 
 // Slices of 2,048 values while all of them together are at most two CTAs an SM (a row's latency counts), else of
-// 16,384 (fewer lists and fixed work for each value).
+// 8,192 (fewer lists and less fixed work for a value).
 cudaError_t work_of(const BeamParams& p, BeamWork* w, int* per) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const long long rows = (long long)p.n * p.beams, small = (p.vocab - 1) / (4 * kRowNT) + 1;
-  *per = rows * small <= 2 * sms ? 4 : 32;
+  *per = rows * small <= 2 * sms ? 4 : 16;
   w->slice_len = *per * kRowNT;
   w->slices = (p.vocab - 1) / w->slice_len + 1;
   return e;
@@ -329,12 +391,16 @@ cudaError_t launch_beam_select(const BeamParams& p, int bf16, void* workspace, c
   w.keys = reinterpret_cast<uint64_t*>(w.sum + lists);
   w.max = reinterpret_cast<float*>(w.keys + lists * p.best);
   const unsigned grid = (unsigned)lists;
-  if (bf16) {
-    if (per == 4) beam_rows_kernel<__nv_bfloat16, 4><<<grid, kRowNT, 0, stream>>>(p, w);
-    else beam_rows_kernel<__nv_bfloat16, 32><<<grid, kRowNT, 0, stream>>>(p, w);
+  const bool even = reinterpret_cast<uintptr_t>(p.logits) % 4 == 0 && p.stride % 2 == 0;
+  if (bf16 && even) {
+    if (per == 4) beam_rows_kernel<__nv_bfloat16, 4, 2><<<grid, kRowNT, 0, stream>>>(p, w);
+    else beam_rows_kernel<__nv_bfloat16, 16, 2><<<grid, kRowNT, 0, stream>>>(p, w);
+  } else if (bf16) {
+    if (per == 4) beam_rows_kernel<__nv_bfloat16, 4, 1><<<grid, kRowNT, 0, stream>>>(p, w);
+    else beam_rows_kernel<__nv_bfloat16, 16, 1><<<grid, kRowNT, 0, stream>>>(p, w);
   } else {
-    if (per == 4) beam_rows_kernel<float, 4><<<grid, kRowNT, 0, stream>>>(p, w);
-    else beam_rows_kernel<float, 32><<<grid, kRowNT, 0, stream>>>(p, w);
+    if (per == 4) beam_rows_kernel<float, 4, 1><<<grid, kRowNT, 0, stream>>>(p, w);
+    else beam_rows_kernel<float, 16, 1><<<grid, kRowNT, 0, stream>>>(p, w);
   }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -407,7 +407,7 @@ typedef struct {
  * A logit of -inf is never selected, nor is NaN; a row with a NaN or +inf, like a dead beam, has no continuation.
  * Where there are fewer than `best`, the rest is -inf, -1, -1.  Totals are compared in fp64: the logits' and scores'
  * numbers as they are, the log sum within 1e-7 of itself; scores_out is rounded once.
- * Scratch, from the library's pool and returned to it in stream order: 12 + 8 * best bytes for each 16,384 entries
+ * Scratch, from the library's pool and returned to it in stream order: 12 + 8 * best bytes for each 8,192 entries
  * of a row (each 2,048 for few rows).  The call can be captured into a graph.  Outputs overlap no input.
  */
 int gdn_beam_select(const gdn_beam_dims* dims, const void* logits, const float* scores, float* scores_out,
