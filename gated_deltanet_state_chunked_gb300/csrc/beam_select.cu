@@ -14,7 +14,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kRowNT = 512, kMergeNT = 256, kMostCandidates = 1024;
+constexpr int kRowNT = 256, kMergeNT = 256, kMostCandidates = 1024;
 
 struct BeamWork {
   double* sum;    // [rows][slices]: sum of exp(x - max) of a slice
@@ -56,22 +56,26 @@ __device__ __forceinline__ uint64_t shfl_xor(uint64_t x, int o) {
 }
 
 // A bound that `best` numbers of the CTA at least reach and few others do: the best-th largest of the maxima of G
-// groups of threads; 0 where fewer groups have a number.  group[0..G) written by the caller.
-template <int G, typename U>
+// groups; 0 where fewer groups have a number.  group[0..G) and *result = 0 are written and visible; NT / G threads share
+// the comparisons of a group.
+template <int NT, int G, typename U>
 __device__ __forceinline__ U bound_of(const U* group, U* result, int best) {
-  if (threadIdx.x == 0) *result = 0;
-  __syncthreads();
-  if (threadIdx.x < G) {
-    const U mine = group[threadIdx.x];
-    int above = 0, same = 0;
-#pragma unroll 16
-    for (int i = 0; i < G; ++i) {
-      const U x = group[i];
-      above += x > mine;
-      same += x == mine;
-    }
-    if (above < best && best <= above + same) *result = mine;  // (several threads write the same)
+  constexpr int kShare = NT / G;
+  const int part = threadIdx.x % kShare;
+  const U mine = group[threadIdx.x / kShare];
+  int above = 0, same = 0;
+#pragma unroll
+  for (int i = part; i < G; i += kShare) {
+    const U x = group[i];
+    above += x > mine;
+    same += x == mine;
   }
+#pragma unroll
+  for (int o = kShare / 2; o; o >>= 1) {
+    above += shfl_xor(above, o);
+    same += shfl_xor(same, o);
+  }
+  if (above < best && best <= above + same) *result = mine;  // (several threads write the same)
   __syncthreads();
   return *result;
 }
@@ -95,28 +99,33 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
-// Place in the slice of a thread's i-th value: one value, or two neighbours, to a load.
+// Place in the slice of a thread's i-th value: VEC neighbours to a load.
 template <int VEC>
 __device__ __forceinline__ int place_of(int i) {
-  return VEC == 2 ? 2 * (threadIdx.x + (i >> 1) * kRowNT) + (i & 1) : threadIdx.x + i * kRowNT;
+  return VEC * (threadIdx.x + i / VEC * kRowNT) + i % VEC;
 }
 
-// PER values a thread, in slices of up to 512 PER.  Bound by HBM where there are many rows: about 9 instructions a value,
-// and several CTAs an SM so that the loads of one cover the work of the others; for few rows by the chain of load, maximum,
-// bound and ranks of one slice.  VEC 2: bf16 rows that start at even places, two values to a load.
+// PER values a thread, in slices of up to 256 PER.  Bound by HBM where there are many rows, with several CTAs an SM so
+// that the loads of one cover the work of the others; for few rows by the chain of load, maximum, bound and ranks of one
+// slice.  VEC values to a load: 16 bytes of rows that are aligned to them (4: fp32, 8: bf16), else 1.
 template <typename T, int PER, int VEC>
-__global__ void __launch_bounds__(kRowNT, 3) beam_rows_kernel(BeamParams p, BeamWork w) {
+__global__ void __launch_bounds__(kRowNT, PER > 16 ? 4 : 6) beam_rows_kernel(BeamParams p, BeamWork w) {
   constexpr int kWarps = kRowNT / 32, kGroups = 2 * kMaxBeams;
   __shared__ __align__(16) uint32_t group[kGroups];
   __shared__ uint32_t bound;
   __shared__ uint64_t cand[kMostCandidates], w_best[kWarps];
-  __shared__ float w_max[kWarps];
+  __shared__ uint32_t w_max[kWarps];
   __shared__ int w_coarse[kWarps], w_fine[kWarps], count, nan;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / w.slices, slice = blockIdx.x - row * w.slices;
@@ -124,43 +133,40 @@ __global__ void __launch_bounds__(kRowNT, 3) beam_rows_kernel(BeamParams p, Beam
   const int v0 = slice * w.slice_len, len = min(p.vocab - v0, w.slice_len);
   const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride + v0;
   float a[PER];
-  if (VEC == 2) {
 #pragma unroll
-    for (int i = 0; i < PER; i += 2) {
-      const int v = place_of<VEC>(i);
-      uint32_t u = 0xff80ff80u;  // -inf, -inf
-      if (v + 1 < len) u = __ldg(reinterpret_cast<const unsigned int*>(x + v));
-      else if (v < len) u = 0xff800000u | __ldg(reinterpret_cast<const unsigned short*>(x + v));
-      a[i] = __uint_as_float(u << 16);
-      a[i + 1] = __uint_as_float(u & 0xffff0000u);
+  for (int i = 0; i < PER; i += VEC) {
+    const int v = place_of<VEC>(i);
+    if (VEC > 1 && v + VEC <= len) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + v));
+      const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        a[i + e] = __uint_as_float(sizeof(T) == 4 ? y[e % 4] : e & 1 ? y[e / 2] & 0xffff0000u : y[e / 2] << 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) a[i + e] = v + e < len ? load_f(x + v + e) : -CUDART_INF_F;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) a[i] = place_of<VEC>(i) < len ? load_f(x + place_of<VEC>(i)) : -CUDART_INF_F;
   }
   float top = -CUDART_INF_F;
 #pragma unroll
   for (int i = 0; i < PER; ++i) top = fmaxf(top, a[i]);
   const uint32_t mine = order_of(top);
-  // (up to 32 continuations are bounded by the maxima of 64 groups of 8 threads, more by those of 128 groups of 4)
+  // (up to 32 continuations are bounded by the maxima of 64 groups of 4 threads, more by those of 128 groups of 2)
   uint32_t g = max(mine, shfl_xor(mine, 1));
-  g = max(g, shfl_xor(g, 2));
   const bool few = p.best <= kMaxBeams / 2;
-  if (few) g = max(g, shfl_xor(g, 4));
-  if ((lane & (few ? 7 : 3)) == 0) group[tid >> (few ? 3 : 2)] = g;
-  float m = top;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, shfl_xor(m, o));
-  if (lane == 0) w_max[warp] = m;
-  if (tid == 0) count = nan = 0;
+  if (few) g = max(g, shfl_xor(g, 2));
+  if ((lane & (few ? 3 : 1)) == 0) group[tid >> (few ? 2 : 1)] = g;
+  g = __reduce_max_sync(0xffffffffu, mine);
+  if (lane == 0) w_max[warp] = g;
+  if (tid == 0) count = nan = bound = 0;
   __syncthreads();
-  m = w_max[0];
 #pragma unroll
-  for (int i = 1; i < kWarps; ++i) m = fmaxf(m, w_max[i]);
+  for (int i = 0; i < kWarps; ++i) g = max(g, w_max[i]);
+  const float m = g ? value_of(g) : -CUDART_INF_F;
   // The sum: each exponential's whole multiples of 2^-16 and what is left of it are added up apart.  A thread's additions
-  // of multiples are exact, and so are the threads' sums as integers (of 2^-16: at most 512 PER 2^16 <= 2^29; of 2^-33).
+  // of multiples are exact, and so are a warp's sums as integers (of 2^-16: at most 32 PER 2^16; of 2^-33: as much).
   {
-    static_assert(PER <= 16, "sums as 32-bit integers");
+    static_assert(PER <= 32, "sums as 32-bit integers");
     const float ref = m == -CUDART_INF_F ? 0.f : m;
     const uint64_t mm = pair(-ref, -ref), log2e = pair(1.4426950408889634f, 1.4426950408889634f);
     const uint64_t up = pair(192.f, 192.f), down = pair(-192.f, -192.f);  // (in [2^7, 2^8): steps of 2^-16)
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(kRowNT, 3) beam_rows_kernel(BeamParams p, Beam
       unpair(mul2(add2(pair(a[i], a[i + 1]), mm), log2e), t0, t1);
       const uint64_t e = pair(exp2_fast(t0), exp2_fast(t1)), c = add2(add2(e, up), down);
       coarse = add2(coarse, c);
-      fine = add2(fine, add2(e, mul2(c, minus)));
+      fine = add2(fine, fma2(c, minus, e));
     }
     float c0, c1, f0, f1;
     unpair(coarse, c0, c1);
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(kRowNT, 3) beam_rows_kernel(BeamParams p, Beam
       w_fine[warp] = fi;
     }
   }
-  const uint32_t least = few ? bound_of<kGroups / 2>(group, &bound, p.best) : bound_of<kGroups>(group, &bound, p.best);
+  const uint32_t least = few ? bound_of<kRowNT, kGroups / 2>(group, &bound, p.best) : bound_of<kRowNT, kGroups>(group, &bound, p.best);
   if (tid == 0) {
     long long c = 0, f = 0;
     for (int i = 0; i < kWarps; ++i) {
@@ -197,10 +203,11 @@ __global__ void __launch_bounds__(kRowNT, 3) beam_rows_kernel(BeamParams p, Beam
     w.sum[blockIdx.x] = nan ? CUDART_NAN : (double)((c << 17) + f) * 0x1p-33;
     w.max[blockIdx.x] = m;
   }
-  if (mine >= least) {
+  const float floor = least ? value_of(least) : -3.402823466e38f;
+  if (top >= floor) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (order_of(a[i]) >= least) {
+      if (a[i] >= floor) {
         const int v = place_of<VEC>(i);
         const uint64_t k = v < len ? key_of(a[i], v0 + v) : 0ull;
         if (k) {
@@ -247,12 +254,13 @@ __global__ void __launch_bounds__(kRowNT, 3) beam_rows_kernel(BeamParams p, Beam
 // A request's candidates are its beams' slices' lists: candidate i is entry i % best of list i / best, a beam's lists side
 // by side.  Of equal totals the lower beam stands first, and within a beam the larger key.
 __global__ void __launch_bounds__(kMergeNT, 3) beam_merge_kernel(BeamParams p, BeamWork w) {
-  constexpr int kGroups = kMergeNT / 4, kWarps = kMergeNT / 32;
+  constexpr int kGroups = 64, kWarps = kMergeNT / 32;
   __shared__ double base[kMaxBeams];
-  __shared__ uint64_t group[kGroups], bound, total[kMostCandidates], w_total[kWarps];
+  __shared__ unsigned long long group[kGroups], bound;
+  __shared__ uint64_t total[kMostCandidates], w_total[kWarps];
   __shared__ int where[kMostCandidates], w_where[kWarps], count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, req = blockIdx.x;
-  const int per_beam = w.slices * p.best, n_all = p.beams * per_beam;
+  const int per_beam = w.slices * p.best, lists = p.beams * w.slices, n_all = lists * p.best;
   tc::grid_dep_wait();
   const size_t first = (size_t)req * p.beams * w.slices;
   const uint64_t* keys = w.keys + first * p.best;
@@ -271,7 +279,8 @@ __global__ void __launch_bounds__(kMergeNT, 3) beam_merge_kernel(BeamParams p, B
     for (int o = 16; o; o >>= 1) s += shfl_xor(s, o);
     if (lane == 0) base[b] = (double)p.scores[(size_t)req * p.beams + b] - ((double)m + log(s));
   }
-  if (tid == 0) count = 0;
+  if (tid < kGroups) group[tid] = 0;
+  if (tid == 0) count = bound = 0;
   __syncthreads();
   auto total_of = [&](int i) -> uint64_t {
     const uint64_t k = keys[i];
@@ -287,21 +296,18 @@ __global__ void __launch_bounds__(kMergeNT, 3) beam_merge_kernel(BeamParams p, B
     p.parents[out] = t ? i / per_beam : -1;
     p.tokens[out] = t ? (int)~(uint32_t)keys[i] : -1;
   };
-  uint64_t top = 0;
-  for (int i = tid; i < n_all; i += kMergeNT) top = max(top, total_of(i));
-  uint64_t g = max(top, shfl_xor(top, 1));
-  g = max(g, shfl_xor(g, 2));
-  if ((lane & 3) == 0) group[tid >> 2] = g;
-  const uint64_t least = bound_of<kGroups>(group, &bound, p.best);
-  if (top >= least)
-    for (int i = tid; i < n_all; i += kMergeNT) {
-      const uint64_t t = total_of(i);
-      if (t && t >= least) {
-        const int n = atomicAdd(&count, 1);
-        if (n < kMostCandidates) {
-          total[n] = t;
-          where[n] = i;
-        }
+  // the bound from the lists' first entries, then every list from its first entry down to the bound
+  for (int i = tid; i < lists; i += kMergeNT) atomicMax(&group[i % kGroups], (unsigned long long)total_of(i * p.best));
+  __syncthreads();
+  const uint64_t least = bound_of<kMergeNT, kGroups>(group, &bound, p.best);
+  for (int i = tid; i < lists; i += kMergeNT)
+    for (int e = 0; e < p.best; ++e) {
+      const uint64_t t = total_of(i * p.best + e);
+      if (!t || t < least) break;
+      const int n = atomicAdd(&count, 1);
+      if (n < kMostCandidates) {
+        total[n] = t;
+        where[n] = i * p.best + e;
       }
     }
   __syncthreads();
@@ -364,8 +370,8 @@ cudaError_t work_of(const BeamParams& p, BeamWork* w, int* per) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const long long rows = (long long)p.n * p.beams, small = (p.vocab - 1) / (4 * kRowNT) + 1;
-  *per = rows * small <= 2 * sms ? 4 : 16;
+  const long long rows = (long long)p.n * p.beams, small = (p.vocab - 1) / (8 * kRowNT) + 1;
+  *per = rows * small <= 2 * sms ? 8 : 32;
   w->slice_len = *per * kRowNT;
   w->slices = (p.vocab - 1) / w->slice_len + 1;
   return e;
@@ -391,17 +397,12 @@ cudaError_t launch_beam_select(const BeamParams& p, int bf16, void* workspace, c
   w.keys = reinterpret_cast<uint64_t*>(w.sum + lists);
   w.max = reinterpret_cast<float*>(w.keys + lists * p.best);
   const unsigned grid = (unsigned)lists;
-  const bool even = reinterpret_cast<uintptr_t>(p.logits) % 4 == 0 && p.stride % 2 == 0;
-  if (bf16 && even) {
-    if (per == 4) beam_rows_kernel<__nv_bfloat16, 4, 2><<<grid, kRowNT, 0, stream>>>(p, w);
-    else beam_rows_kernel<__nv_bfloat16, 16, 2><<<grid, kRowNT, 0, stream>>>(p, w);
-  } else if (bf16) {
-    if (per == 4) beam_rows_kernel<__nv_bfloat16, 4, 1><<<grid, kRowNT, 0, stream>>>(p, w);
-    else beam_rows_kernel<__nv_bfloat16, 16, 1><<<grid, kRowNT, 0, stream>>>(p, w);
-  } else {
-    if (per == 4) beam_rows_kernel<float, 4, 1><<<grid, kRowNT, 0, stream>>>(p, w);
-    else beam_rows_kernel<float, 16, 1><<<grid, kRowNT, 0, stream>>>(p, w);
-  }
+  const bool wide = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.stride * (bf16 ? 2 : 4) % 16 == 0;
+  auto rows = [&](auto kernel) { kernel<<<grid, kRowNT, 0, stream>>>(p, w); };
+  if (bf16 && wide) rows(per == 8 ? beam_rows_kernel<__nv_bfloat16, 8, 8> : beam_rows_kernel<__nv_bfloat16, 32, 8>);
+  else if (bf16) rows(per == 8 ? beam_rows_kernel<__nv_bfloat16, 8, 1> : beam_rows_kernel<__nv_bfloat16, 32, 1>);
+  else if (wide) rows(per == 8 ? beam_rows_kernel<float, 8, 4> : beam_rows_kernel<float, 32, 4>);
+  else rows(per == 8 ? beam_rows_kernel<float, 8, 1> : beam_rows_kernel<float, 32, 1>);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
