@@ -88,13 +88,17 @@ cudaError_t launch_join(const PagedParams& p, int bf16, const Scratch& s, int G,
 
 }  // namespace paged
 
+// bf16: up to 16 rows a key head (single tokens) leave 128-row products nearly empty and need bytes under way; pages that have no tensor
+// map (fewer than 8 tokens, strides that it does not take) fall to the CUDA cores, as fp32 does.
 cudaError_t paged_workspace_bytes(const PagedParams& p, int bf16, size_t* bytes) {
-  if (!bf16) return paged::simt_workspace(p, bf16, bytes);
-  return paged::split_supported(p) ? paged::split_workspace(p, bytes) : paged::tc_workspace(p, bytes);
+  if (bf16 && paged::split_supported(p)) return paged::split_workspace(p, bytes);
+  if (bf16 && paged::tc_supported(p)) return paged::tc_workspace(p, bytes);
+  return paged::simt_workspace(p, bf16, bytes);
 }
 cudaError_t launch_paged_attn(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream) {
-  if (!bf16) return paged::launch_simt(p, bf16, workspace, stream);
-  return paged::split_supported(p) ? paged::launch_split(p, workspace, stream) : paged::launch_tc(p, workspace, stream);
+  if (bf16 && paged::split_supported(p)) return paged::launch_split(p, workspace, stream);
+  if (bf16 && paged::tc_supported(p)) return paged::launch_tc(p, workspace, stream);
+  return paged::launch_simt(p, bf16, workspace, stream);
 }
 
 }  // namespace gdn

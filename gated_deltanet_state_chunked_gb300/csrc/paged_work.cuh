@@ -371,6 +371,7 @@ cudaError_t launch_join(const PagedParams& p, int bf16, const Scratch& s, int G,
 cudaError_t launch_simt(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream);
 cudaError_t simt_workspace(const PagedParams& p, int bf16, size_t* bytes);
 cudaError_t launch_tc(const PagedParams& p, void* workspace, cudaStream_t stream);
+bool tc_supported(const PagedParams& p);
 bool split_supported(const PagedParams& p);
 cudaError_t launch_split(const PagedParams& p, void* workspace, cudaStream_t stream);
 cudaError_t split_workspace(const PagedParams& p, size_t* bytes);
