@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(NT, 2) paged_split_kernel(const PagedParams p,
     // ---- the item's end
     const bool whole = n == w.units;
     if (tid == 0 && w.at == 0 && !whole)
-      s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.cta_of(w.pos + w.units - 1)};
+      s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta()};
     const size_t slot_row = (size_t)(w.at ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * (16 * MT);
     if (tid < 16 * MT) again[tid] = 0;
 #pragma unroll

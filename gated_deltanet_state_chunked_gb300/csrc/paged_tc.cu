@@ -13,7 +13,7 @@
 //
 // Warps: 0-3 and 4-7 the halves' rows, a thread a row: maximum, exponentials, P.  8-11 the outputs: an item's O goes
 // from TMEM into registers at once, so that the next item's products can begin, and is stored beside them.  12 issues
-// the MMAs.  13 loads Q, and K and V into a ring of five 32 KB stages, by tensor copies (a page at a time, up to 128 rows of it).
+// the MMAs.  13 loads Q and K, 14 V, into a ring of five 32 KB stages, by tensor copies (a page at a time, up to 128 rows of it).
 // The rows of V behind a request's end (they may hold anything) are cleared before they are handed on.  Registers are
 // moved from the last eight warps to the rows'.  Every hand-off is an mbarrier; every wait is bounded.
 #include <atomic>
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(NT, 1)
         }
       }
       if (tid == 256 && w.at == 0 && !whole)
-        s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.cta_of(w.pos + w.units - 1)};
+        s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta()};
       w.advance(p, tile_tokens, n);
     }
   } else {
@@ -480,54 +480,48 @@ __global__ void __launch_bounds__(NT, 1)
       if (elect_one()) mma_commit(&bar[kDrain]);
       __syncwarp();
       mbar_wait(&bar[kDrain], 0, kWaitNs);
-    } else if (quad == 1) {
-      // ---------------------------------------------------------- loads
+    } else if (quad < 3) {
+      // ---------------------------------------------------------- loads: warp 13 Q and K, warp 14 V
       const uint32_t base = smem_u32(sm);
+      const bool values = quad == 2;
+      const CUtensorMap* map = values ? &map_v : &map_k;
+      const PageMap m = values ? mv : mk;
       const int mask = (1 << p.page_shift) - 1, atoms = p.d > 64 ? 2 : 1;
-      const int boxes = BN / mk.rows, box = lane & (boxes - 1), atom = lane / boxes;  // this lane's box of a stage
-      int issued = 0, items = 0, tails = 0;
+      const int boxes = BN / m.rows, box = lane & (boxes - 1), atom = lane / boxes;  // this lane's box of a stage
+      int g = values ? 1 : 0, items = 0, tails = 0;  // the next stage (every other one), items, tails
       bool ok = true;
       while (w.left > 0 && ok) {
         const int n = w.step(), first = (w.span.lo / BN + w.at) * BN;
         const Span span = w.span;
         // the page of this lane's box of unit u: outside the cache (where a copy reads zeros) if no key of it is wanted
         auto page_at = [&](int u) {
-          const int j = first + u * BN + box * mk.rows;
-          const int page = u < n && j < span.hi && j + mk.rows > span.lo ? page_of(p, w.req, j) : -1;
+          const int j = first + u * BN + box * m.rows;
+          const int page = u < n && j < span.hi && j + m.rows > span.lo ? page_of(p, w.req, j) : -1;
           return page < 0 ? p.n_pages : page;
         };
-        // A stage: its copies count on barrier b.
-        auto copy = [&](const CUtensorMap* map, const PageMap& m, int u, int page, int b) {
-          const int st = issued % kStages;
-          if (issued >= kStages && !(ok = wait(kEmpty + st, issued / kStages - 1, kLongNs))) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&bar[b < 0 ? kFull + st : b], (uint32_t)BN * 128u * atoms);
+        int page = page_at(0);
+        for (int u = 0; u < n; ++u, g += 2) {
+          const int st = g % kStages, live = w.r.kv - (first + u * BN);  // rows of the unit before the request's end
+          const bool tail = values && live < BN;
+          const int b = tail ? kTail : kFull + st;
+          if (g >= kStages && !(ok = wait(kEmpty + st, g / kStages - 1, kLongNs))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bar[b], (uint32_t)BN * 128u * atoms);
           __syncwarp();
           if (lane < boxes * atoms)
-            tma_load_page(base + kRing + st * kTile + atom * kAtom + box * mk.rows * 128, map, m, &bar[b < 0 ? kFull + st : b], 64 * atom,
-                          (first + u * BN + box * mk.rows) & mask, w.head, page);
+            tma_load_page(base + kRing + st * kTile + atom * kAtom + box * m.rows * 128, map, m, &bar[b], 64 * atom,
+                          (first + u * BN + box * m.rows) & mask, w.head, page);
           __syncwarp();
-          ++issued;
-          return true;
-        };
-        int page = page_at(0);
-        for (int u = 0; u < n; ++u) {
-          const int live = w.r.kv - (first + u * BN);  // rows of the unit before the request's end
-          const int here = page;
-          if (!copy(&map_k, mk, u, here, -1)) break;
           page = page_at(u + 1);
-          if (!copy(&map_v, mv, u, here, live >= BN ? -1 : kTail)) break;
-          if (u == 0) {
+          if (u == 0 && !values) {
             if (items > 0 && !(ok = wait(kQEmpty, items - 1, kLongNs))) break;
-            const int rows = p.group * tile_tokens;
-            if (lane == 0) mbar_arrive_expect_tx(&bar[kQFull], (uint32_t)rows * 128u * atoms);
+            if (lane == 0) mbar_arrive_expect_tx(&bar[kQFull], (uint32_t)(p.group * tile_tokens) * 128u * atoms);
             __syncwarp();
             if (lane < atoms)
               tma_load_3d(base + kQ + lane * kQAtom, &map_q, &bar[kQFull], 64 * lane, w.head * p.group, w.r.q0 + w.tile * tile_tokens);
             __syncwarp();
           }
-          if (live < BN) {
+          if (tail) {
             if (!(ok = wait(kTail, tails++))) break;
-            const int st = (issued - 1) % kStages;
             for (int i = max(live, 0) * 8 + lane; i < BN * 8; i += 32)
               for (int a = 0; a < atoms; ++a)
                 *reinterpret_cast<uint4*>(sm + kRing + st * kTile + a * kAtom + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
@@ -540,9 +534,9 @@ __global__ void __launch_bounds__(NT, 1)
         w.advance(p, tile_tokens, n);
       }
       if (!ok) {  // let the copies in flight land
-        for (int i = max(0, issued - kStages); i < issued; ++i)
+        for (int i = max(values ? 1 : 0, g - 2 * kStages); i < g; i += 2)
           mbar_wait(&bar[kFull + i % kStages], (uint32_t)((i / kStages) & 1), kWaitNs / 100);
-        mbar_wait(&bar[kQFull], (uint32_t)(items & 1), kWaitNs / 100);
+        if (!values) mbar_wait(&bar[kQFull], (uint32_t)(items & 1), kWaitNs / 100);
       }
     }
   }
