@@ -39,7 +39,7 @@ static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t cS = 0, cO = 256;  // TMEM columns of the halves' S (and P) and O, 128 each
 constexpr uint64_t kLongNs = 2 * kWaitNs;  // waits that rows computed again may hold up
 
-enum Bar { kFull = 0, kEmpty = kFull + kStages, kQFull = kEmpty + kStages, kQEmpty, kTail, kDrain, kS, kP = kS + 2, kO = kP + 2,
+enum Bar { kFull = 0, kEmpty = kFull + kStages, kQFull = kEmpty + kStages, kQEmpty, kTail, kDrain, kS, kP = kS + 2 /* by columns: 0-63, 64-127 */, kO = kP + 4,
            kStat = kO + 2, kOFree = kStat + 2, kBars = kOFree + 2 };
 static_assert(kBars * 8 <= 256, "barrier area");
 
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(NT, 1)
   }
   if (tid == 32) {
     for (int b = 0; b < kBars; ++b)
-      mbar_init(&bar[b], (b >= kP && b < kP + 2) || (b >= kStat && b < kOFree + 2) ? 4 : 1);
+      mbar_init(&bar[b], (b >= kP && b < kP + 4) || (b >= kStat && b < kOFree + 2) ? 4 : 1);
     mbar_fence_init();
     *dead = 0;
     s.shared[blockIdx.x].req = -1;
@@ -258,13 +258,15 @@ __global__ void __launch_bounds__(NT, 1)
               o[j / 2] = pack_bf16(e0, e1);
             }
             tmem_st16(at_s + 16 * i, o);
+            if (i & 1) {  // (half of P is multiplied while the other half is made)
+              tmem_st_wait();
+              tc_fence_before();
+              arrive(kP + group + (i & 2));
+            }
           }
           float y0, y1;
           unpair(add2(sum[0], sum[1]), y0, y1);
           l += y0 + y1;
-          tmem_st_wait();
-          tc_fence_before();
-          arrive(kP + group);
         }
         if (!ok) break;
         if (items > 0 && !(ok = wait(kOFree + group, items - 1, kLongNs))) break;  // (the item before it has been read)
@@ -409,27 +411,31 @@ __global__ void __launch_bounds__(NT, 1)
         }
         __syncwarp();
       };
-      auto pv = [&](int h, int st, bool add, bool free) {
-        if (elect_one()) {
-          const uint64_t v = dV + (uint64_t)((st * kTile) >> 4);
-#pragma unroll
-          for (int i = 0; i < BN / 16; ++i)
-            mma_bf16_ts(tmem + cO + 128 * h, tmem + cS + 128 * h + 8 * i, v + (uint64_t)((i * 2048) >> 4), idPV, add || i > 0);
-          mma_commit(&bar[kO + h]);
-          if (free) mma_commit(&bar[kEmpty + st]);
-        }
-        __syncwarp();
-      };
       int g = 0, items = 0;                       // stages taken, items
       int units[2] = {0, 0}, outs[2] = {0, 0};    // units and items of the halves
       bool ok = true;
       auto full = [&](int i) { return wait(kFull + i % kStages, i / kStages, kLongNs); };
-      // P of the half's next unit is there, and (first) the outputs of its item before have been read
-      auto weights = [&](int h, bool first) {
-        if (!wait(kP + h, units[h], kLongNs)) return false;
-        if (first && outs[h] > 0 && !wait(kOFree + h, outs[h] - 1, kLongNs)) return false;
+      // O (+)= P V of the half's next unit, by halves of P as they come; before an item's first, the outputs of the
+      // half's item before have been read
+      auto pv = [&](int h, int st, bool first, bool free) {
+        const uint64_t v = dV + (uint64_t)((st * kTile) >> 4);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(kP + h + 2 * half, units[h], kLongNs)) return false;
+          if (half == 0 && first && outs[h] > 0 && !wait(kOFree + h, outs[h] - 1, kLongNs)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 4 * half; i < 4 * half + 4; ++i)
+              mma_bf16_ts(tmem + cO + 128 * h, tmem + cS + 128 * h + 8 * i, v + (uint64_t)((i * 2048) >> 4), idPV, !first || i > 0);
+            if (half == 1) {
+              mma_commit(&bar[kO + h]);
+              if (free) mma_commit(&bar[kEmpty + st]);
+            }
+          }
+          __syncwarp();
+        }
         ++units[h];
-        tc_fence_after();
         return true;
       };
       while (w.left > 0 && ok) {
@@ -446,8 +452,7 @@ __global__ void __launch_bounds__(NT, 1)
           }
           for (int u = 0; u < n; ++u) {
             const int h = u & 1, sv = g + 2 * u + 1, sk = g + 2 * u + 4;
-            if (!(ok = full(sv) && weights(h, u < 2))) break;
-            pv(h, sv % kStages, u > 1, true);
+            if (!(ok = full(sv) && pv(h, sv % kStages, u < 2, true))) break;
             if (u + 2 < n) {
               if (!(ok = full(sk))) break;
               tc_fence_after();
@@ -460,8 +465,7 @@ __global__ void __launch_bounds__(NT, 1)
             const int sv = g + 2 * u + 1, sk = g + 2 * u + 2;
             if (!(ok = full(sv))) break;
             for (int h = 0; h < 2; ++h) {
-              if (!(ok = weights(h, u == 0))) break;
-              pv(h, sv % kStages, u > 0, h == 1);
+              if (!(ok = pv(h, sv % kStages, u == 0, h == 1))) break;
               if (u + 1 < n) {
                 if (h == 0) {
                   if (!(ok = full(sk))) break;
