@@ -6,9 +6,12 @@ namespace paged {
 namespace {
 
 // One CTA of 256 threads, tiles of BM = 16 TR query rows x 64 keys.  Thread (ty, tx) = (tid / 16, tid % 16)
-// holds rows TR ty .. and keys tx + 16 j of the scores, columns 4 tx + 64 j of the outputs.  Keys and values each
-// have one buffer: the next tile's keys arrive while the values are multiplied, its values while the scores are.
+// holds rows TR ty .. and keys tx + 16 j of the scores, columns 2 tx + 32 j (and the next) of the outputs, as pairs for the
+// packed FMAs (two products in one instruction; the scores' pairs are even and odd places of the head).  Keys and values
+// each have one buffer: the next tile's keys arrive while the values are multiplied, its values while the scores are.
+// Bound by the FMA pipe: BENCH
 constexpr int NT = 256, BN = 64, LDP = BN + 4;
+constexpr int COST = 0;  // (of an item, in units: a unit takes 13 us, the rest of an item 4)
 
 __device__ __forceinline__ void cp16(void* dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
@@ -30,6 +33,27 @@ __device__ __forceinline__ void put4(float* dst, const __nv_bfloat16* src, bool 
                __uint_as_float(u.y & 0xffff0000u)};
   }
   *reinterpret_cast<float4*>(dst) = v;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
 }
 
 template <typename T>
@@ -56,7 +80,7 @@ struct Smem {
 };
 
 template <typename T, int TR>
-__global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s, int tile_tokens) {
+__global__ void __launch_bounds__(NT, TR <= 2 ? 2 : 1) paged_simt_kernel(PagedParams p, Scratch s, int tile_tokens) {
   constexpr int BM = 16 * TR;
   extern __shared__ __align__(16) float smem[];
   __shared__ PlanSmem plan_sm;
@@ -65,8 +89,8 @@ __global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s
   const int ld = p.d + 4;
   float *Q = smem, *K = Q + BM * ld, *V = K + BN * ld, *P = V + BN * ld;
   tc::grid_dep_launch();
-  Walk<BN> w;
-  const bool work = plan<BN, NT>(p, tile_tokens, plan_sm, w);
+  Walk<BN, COST> w;
+  const bool work = plan<BN, COST, NT>(p, tile_tokens, plan_sm, w);
   if (tid == 0) s.shared[blockIdx.x].req = -1;
   if (!work) return;
   const float s2 = p.scale * kLog2e;
@@ -88,12 +112,13 @@ __global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s
     cp_commit();
     load_tile(p, V, ld, vp, p.v_page, p.v_token, w.req, first, w.span);
     cp_commit();
-    float o[TR][8], m[TR], l[TR];
+    uint64_t o[TR][4];
+    float m[TR], l[TR];
     int lo[TR], hi[TR];  // keys that the rows see
 #pragma unroll
     for (int i = 0; i < TR; ++i) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) o[i][c] = 0.f;
+      for (int c = 0; c < 4; ++c) o[i][c] = 0ull;
       m[i] = -CUDART_INF_F;
       l[i] = 0.f;
       const Row x = row_of(p, rq, w.head, w.tile, tile_tokens, ty * TR + i);
@@ -101,35 +126,45 @@ __global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s
       hi[i] = x.live ? pos + 1 : 0;
       lo[i] = p.window ? max(0, pos - p.window + 1) : 0;
     }
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < TR; ++i) any |= hi[i] > 0;
+    const bool busy = __any_sync(0xffffffffu, any);  // (a warp whose rows are none, or see nothing, has only loads to do)
     for (int u = 0; u < n; ++u) {
       const int j0 = first + u * BN;
       cp_wait<1>();
       __syncthreads();
       float a[TR][4];
+      if (busy) {
+        uint64_t acc[TR][4];
 #pragma unroll
-      for (int i = 0; i < TR; ++i)
+        for (int i = 0; i < TR; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[i][j] = 0.f;
+          for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
 #pragma unroll 2
-      for (int x = 0; x < p.d; x += 4) {
-        float4 kk[4];
+        for (int x = 0; x < p.d; x += 4) {
+          ulonglong2 kk[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(K + (tx + 16 * j) * ld + x);
+          for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const ulonglong2*>(K + (tx + 16 * j) * ld + x);
 #pragma unroll
-        for (int i = 0; i < TR; ++i) {
-          const float4 q = *reinterpret_cast<const float4*>(Q + (ty * TR + i) * ld + x);
+          for (int i = 0; i < TR; ++i) {
+            const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(Q + (ty * TR + i) * ld + x);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[i][j] = fmaf(q.x, kk[j].x, a[i][j]);
-            a[i][j] = fmaf(q.y, kk[j].y, a[i][j]);
-            a[i][j] = fmaf(q.z, kk[j].z, a[i][j]);
-            a[i][j] = fmaf(q.w, kk[j].w, a[i][j]);
+            for (int j = 0; j < 4; ++j) acc[i][j] = fma2(q.y, kk[j].y, fma2(q.x, kk[j].x, acc[i][j]));
           }
         }
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = unpair(acc[i][j]);
+            a[i][j] = y.x + y.y;
+          }
       }
       __syncthreads();
       if (u + 1 < n) load_tile(p, K, ld, kp, p.k_page, p.k_token, w.req, j0 + BN, w.span);
       cp_commit();
+      if (busy) {
 #pragma unroll
       for (int i = 0; i < TR; ++i) {
         float top = -CUDART_INF_F;
@@ -154,35 +189,33 @@ __global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s
         for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         l[i] = fmaf(l[i], shrink, sum);
         m[i] = m_new;
+        const uint64_t ss = pair(shrink, shrink);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) o[i][c] *= shrink;
+        for (int c = 0; c < 4; ++c) o[i][c] = mul2(o[i][c], ss);
+      }
       }
       cp_wait<1>();
       __syncthreads();
-      const bool second = 64 + tx * 4 < p.d, one = tx * 4 < p.d;
-#pragma unroll 2
-      for (int x = 0; x < BN; x += 4) {
+      const int cols = (p.d + 31) / 32;  // (places behind d in the last columns: what the buffer holds there, not stored)
+#pragma unroll 1
+      for (int x = 0; x < (busy ? BN : 0); x += 4) {
         float4 pr[TR];
 #pragma unroll
         for (int i = 0; i < TR; ++i) pr[i] = *reinterpret_cast<const float4*>(P + (ty * TR + i) * LDP + x);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          float4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
-          if (one) v0 = *reinterpret_cast<const float4*>(V + (x + y) * ld + tx * 4);
-          if (second) v1 = *reinterpret_cast<const float4*>(V + (x + y) * ld + 64 + tx * 4);
+        for (int j = 0; j < 4; ++j)
+          if (j < cols) {
+            uint64_t v[4];
 #pragma unroll
-          for (int i = 0; i < TR; ++i) {
-            const float e = y == 0 ? pr[i].x : y == 1 ? pr[i].y : y == 2 ? pr[i].z : pr[i].w;
-            o[i][0] = fmaf(e, v0.x, o[i][0]);
-            o[i][1] = fmaf(e, v0.y, o[i][1]);
-            o[i][2] = fmaf(e, v0.z, o[i][2]);
-            o[i][3] = fmaf(e, v0.w, o[i][3]);
-            o[i][4] = fmaf(e, v1.x, o[i][4]);
-            o[i][5] = fmaf(e, v1.y, o[i][5]);
-            o[i][6] = fmaf(e, v1.z, o[i][6]);
-            o[i][7] = fmaf(e, v1.w, o[i][7]);
+            for (int y = 0; y < 4; ++y) v[y] = *reinterpret_cast<const uint64_t*>(V + (x + y) * ld + 32 * j + 2 * tx);
+#pragma unroll
+            for (int i = 0; i < TR; ++i) {
+              o[i][j] = fma2(pair(pr[i].x, pr[i].x), v[0], o[i][j]);
+              o[i][j] = fma2(pair(pr[i].y, pr[i].y), v[1], o[i][j]);
+              o[i][j] = fma2(pair(pr[i].z, pr[i].z), v[2], o[i][j]);
+              o[i][j] = fma2(pair(pr[i].w, pr[i].w), v[3], o[i][j]);
+            }
           }
-        }
       }
       __syncthreads();
       if (u + 1 < n) load_tile(p, V, ld, vp, p.v_page, p.v_token, w.req, j0 + BN, w.span);
@@ -199,26 +232,21 @@ __global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s
       if (!x.live) continue;
       const bool sees = whole ? hi[i] > 0 : l[i] != 0.f;
       const float f = row_factor(l[i], sees);
+      const size_t out = (size_t)(rq.q0 + x.t) * p.h_q + x.h;
       bool fine = true;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        o[i][c] = sees ? o[i][c] * f : 0.f;
-        fine = fine && fabsf(o[i][c]) <= 3.402823466e38f;
-      }
-      const size_t out = (size_t)(rq.q0 + x.t) * p.h_q + x.h;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = 64 * j + tx * 4;
+      for (int j = 0; j < 4; ++j) {
+        const int c = 32 * j + 2 * tx;
         if (c >= p.d) continue;
-        const float4 v = {o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+        float2 v = unpair(o[i][j]);
+        v = sees ? float2{v.x * f, v.y * f} : float2{0.f, 0.f};
+        fine = fine && fabsf(v.x) <= 3.402823466e38f && fabsf(v.y) <= 3.402823466e38f;
         if (!whole) {
-          *reinterpret_cast<float4*>(s.rows + (slot + r) * p.d + c) = v;
+          *reinterpret_cast<float2*>(s.rows + (slot + r) * p.d + c) = v;
         } else if (sizeof(T) == 4) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.O) + out * p.d + c) = v;
+          *reinterpret_cast<float2*>(static_cast<float*>(p.O) + out * p.d + c) = v;
         } else {
-          __nv_bfloat162 y = __floats2bfloat162_rn(v.x, v.y), z = __floats2bfloat162_rn(v.z, v.w);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + out * p.d + c) =
-              uint2{*reinterpret_cast<uint32_t*>(&y), *reinterpret_cast<uint32_t*>(&z)};
+          *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.O) + out * p.d + c) = __floats2bfloat162_rn(v.x, v.y);
         }
       }
       if (tx == 0) {
@@ -236,14 +264,14 @@ __global__ void __launch_bounds__(NT) paged_simt_kernel(PagedParams p, Scratch s
   }
 }
 
-// Rows of a tile: 16 where a request's rows fit (short windows: two CTAs an SM), 64, 128 otherwise (its thread
-// tile of 8 rows x 4 keys takes half as much shared memory traffic for a product as 4 x 4).
+// Rows of a tile: the fewest of 16, 32, 64 and 128 that hold a request's (the thread tile of 8 rows x 4 keys takes half as
+// much shared memory traffic for a product as 4 x 4); up to 32 two CTAs an SM fit, whose loads cover each other's work.
 struct Shape {
   int tr, ctas;
 };
 Shape shape_of(const PagedParams& p) {
   const long long rows = (long long)p.max_q * p.group;
-  return rows <= 16 ? Shape{1, 2} : rows <= 64 ? Shape{4, 1} : Shape{8, 1};
+  return rows <= 16 ? Shape{1, 2} : rows <= 32 ? Shape{2, 2} : rows <= 64 ? Shape{4, 1} : Shape{8, 1};
 }
 
 template <typename T, int TR>
@@ -272,14 +300,14 @@ cudaError_t launch_simt(const PagedParams& p, int bf16, void* workspace, cudaStr
   const Shape sh = shape_of(p);
   const int G = sms * sh.ctas, BM = 16 * sh.tr, tile_tokens = BM / p.group;
   const Scratch s = scratch_at(workspace, G, BM, p.d);
-  if (bf16)
-    e = sh.tr == 1   ? launch<__nv_bfloat16, 1>(p, s, G, tile_tokens, stream)
-        : sh.tr == 4 ? launch<__nv_bfloat16, 4>(p, s, G, tile_tokens, stream)
-                     : launch<__nv_bfloat16, 8>(p, s, G, tile_tokens, stream);
-  else
-    e = sh.tr == 1   ? launch<float, 1>(p, s, G, tile_tokens, stream)
-        : sh.tr == 4 ? launch<float, 4>(p, s, G, tile_tokens, stream)
-                     : launch<float, 8>(p, s, G, tile_tokens, stream);
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    return sh.tr == 1   ? launch<T, 1>(p, s, G, tile_tokens, stream)
+           : sh.tr == 2 ? launch<T, 2>(p, s, G, tile_tokens, stream)
+           : sh.tr == 4 ? launch<T, 4>(p, s, G, tile_tokens, stream)
+                        : launch<T, 8>(p, s, G, tile_tokens, stream);
+  };
+  e = bf16 ? run(__nv_bfloat16()) : run(0.f);
   return e != cudaSuccess ? e : launch_join(p, bf16, s, G, BM, tile_tokens, stream);
 }
 

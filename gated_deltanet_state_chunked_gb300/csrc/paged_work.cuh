@@ -3,12 +3,12 @@
 // An item is one (request, key head, row tile): the query rows of up to `tile_tokens` consecutive new
 // tokens, all the query heads of the key head, against the keys that any of them sees, in units of BN keys
 // (an item that sees no key is one unit).  The items of a call, request after request, head after head, form one line of
-// units, kItemCost places for what an item costs besides ahead of each one's, and each of G CTAs takes an equal stretch
-// of the line, whatever the lengths are: lengths are read on the device, so that no host code could deal the items out,
-// and a long request next to short ones fills the GPU.  (Without those places a CTA that met eleven short items
-// took 147 us where the others took 119: 64 tokens over up to 6,000 keys.)  An item that several CTAs share leaves partial
-// results (normalised rows, running maximum and sum) in scratch, which paged_join_kernel puts together in the order
-// of the keys: results do not depend on timing.
+// units, COST places ahead of each one's for what an item costs besides (its queries, the filling and draining of the
+// pipeline, its outputs), and each of G CTAs takes an equal stretch of the line, whatever the lengths are: lengths are
+// read on the device, so that no host code could deal the items out, and a long request next to short ones fills the
+// GPU.  (Without those places a CTA that met eleven short items took 147 us where the others took 119: 64 tokens over
+// up to 6,000 keys.)  An item that several CTAs share leaves partial results (normalised rows, running maximum and
+// sum) in scratch, which paged_join_kernel puts together in the order of the keys: results do not depend on timing.
 #pragma once
 
 #include <climits>
@@ -45,9 +45,6 @@ inline Scratch scratch_at(void* ws, int G, int BM, int d) {
   s.shared = reinterpret_cast<Shared*>(s.stat + (size_t)2 * G * BM);
   return s;
 }
-
-// What an item costs besides its units, in units: its queries, the filling and draining of the pipeline, its outputs.
-constexpr int kItemCost = 2;
 
 // A request: its rows of q, its new tokens (0: nothing to do), its tokens in the cache.
 struct Request {
@@ -90,7 +87,7 @@ __device__ __forceinline__ int units_of(const Span& s) {
 }
 
 // Walks the stretch of one CTA.  All threads hold the same values.
-template <int BN>
+template <int BN, int COST>
 struct Walk {
   int req, top;    // request, and the largest offset before it
   Request r;
@@ -112,9 +109,9 @@ struct Walk {
     left -= n;
     at += n;
     if (at < units) return;  // (the stretch ends inside the item)
-    left -= kItemCost;
+    left -= COST;
     if (left <= 0) return;
-    begin += kItemCost + units;
+    begin += COST + units;
     at = 0;
     if ((tile + 1) * tile_tokens < r.len) {
       ++tile;
@@ -133,7 +130,7 @@ struct Walk {
     set_tile(p, tile_tokens);
   }
   // The CTA that works on the item's last unit.
-  __device__ __forceinline__ int last_cta() const { return (int)(((begin + kItemCost + units) * G - 1) / total); }
+  __device__ __forceinline__ int last_cta() const { return (int)(((begin + COST + units) * G - 1) / total); }
 };
 
 struct PlanSmem {
@@ -143,17 +140,17 @@ struct PlanSmem {
   int req, top_before;
 };
 
-template <int BN>
+template <int BN, int COST>
 __device__ __forceinline__ long long request_places(const PagedParams& p, const Request& r, int tile_tokens) {
   long long n = 0;
-  for (int t = 0; t < r.len; t += tile_tokens) n += kItemCost + units_of<BN>(span_of(p, r, t, tile_tokens));
+  for (int t = 0; t < r.len; t += tile_tokens) n += COST + units_of<BN>(span_of(p, r, t, tile_tokens));
   return n * p.h_kv;
 }
 
 // Finds this CTA's stretch: false if it has none.  All NT threads of the CTA call it; CTA 0 reports
 // malformed requests.
-template <int BN, int NT>
-__device__ bool plan(const PagedParams& p, int tile_tokens, PlanSmem& sm, Walk<BN>& w) {
+template <int BN, int COST, int NT>
+__device__ bool plan(const PagedParams& p, int tile_tokens, PlanSmem& sm, Walk<BN, COST>& w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long total = 0, u0 = 0;
   for (int pass = 0; pass < 2; ++pass) {
@@ -180,7 +177,7 @@ __device__ bool plan(const PagedParams& p, int tile_tokens, PlanSmem& sm, Walk<B
       if (i < p.n) {
         bool bad;
         const Request r = request_of(p, i, before, &bad);
-        mine = request_places<BN>(p, r, tile_tokens);
+        mine = request_places<BN, COST>(p, r, tile_tokens);
         if (bad && pass == 0 && blockIdx.x == 0) atomicExch(p.status, GDN_ERR_SHAPE);
       }
       long long incl = mine;
@@ -224,17 +221,17 @@ __device__ bool plan(const PagedParams& p, int tile_tokens, PlanSmem& sm, Walk<B
   bool bad;
   w.r = request_of(p, w.req, w.top, &bad);
   long long u = u0 - sm.start;
-  const long long per_head = request_places<BN>(p, w.r, tile_tokens) / p.h_kv;
+  const long long per_head = request_places<BN, COST>(p, w.r, tile_tokens) / p.h_kv;
   w.head = (int)(u / per_head);
   u -= w.head * per_head;
   for (w.tile = 0;; ++w.tile) {
     w.set_tile(p, tile_tokens);
-    if (u < kItemCost + w.units) break;
-    u -= kItemCost + w.units;
+    if (u < COST + w.units) break;
+    u -= COST + w.units;
   }
   w.begin = u0 - u;
-  w.at = max(0, (int)u - kItemCost);
-  w.left = (int)(end - (w.begin + kItemCost + w.at));  // (a stretch has fewer places than 2^31 units)
+  w.at = max(0, (int)u - COST);
+  w.left = (int)(end - (w.begin + COST + w.at));  // (a stretch has fewer places than 2^31 units)
   return w.left > 0;
 }
 
