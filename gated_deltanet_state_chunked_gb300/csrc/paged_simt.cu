@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(NT, TR <= 2 ? 2 : 1) paged_simt_kernel(PagedPa
     const int first = (w.span.lo / BN + w.at) * BN;  // first key of the first unit
     for (int r = tid; r < BM; r += NT) again[r] = 0;
     if (tid == 0 && w.at == 0 && n < w.units)
-      s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta()};
+      s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta(), rq, 0};
     for (int r = warp; r < BM; r += NT / 32) {
       const Row x = row_of(p, rq, w.head, w.tile, tile_tokens, r);
       const T* q = static_cast<const T*>(p.q) + (x.live ? (int64_t)(rq.q0 + x.t) * p.q_stride + (int64_t)x.h * p.d : 0);

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(NT, 2) paged_split_kernel(const PagedParams p,
     // ---- the item's end
     const bool whole = n == w.units;
     if (tid == 0 && w.at == 0 && !whole)
-      s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta()};
+      s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta(), rq, 0};
     const size_t slot_row = (size_t)(w.at ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * (16 * MT);
     if (tid < 16 * MT) again[tid] = 0;
 #pragma unroll

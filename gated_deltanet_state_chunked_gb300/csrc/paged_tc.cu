@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(NT, 1)
         }
       }
       if (tid == 256 && w.at == 0 && !whole)
-        s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta()};
+        s.shared[blockIdx.x] = Shared{w.req, w.head, w.tile, w.last_cta(), rq, 0};
       w.advance(p, tile_tokens, n);
     }
   } else {

@@ -25,10 +25,17 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// A request: its rows of q, its new tokens (0: nothing to do), its tokens in the cache.
+struct Request {
+  int q0, len, kv;
+};
+
 // Partial results: what CTA c does of an item that an earlier CTA began lies in slot 2 c, its part of one that it
 // begins and does not finish in slot 2 c + 1.
 struct Shared {
   int req, head, tile, last;  // an item that CTA c began and CTA `last` finished; req < 0: none
+  Request r;
+  int pad;
 };
 struct Scratch {
   float* rows;   // [2 G][BM][d]
@@ -46,10 +53,6 @@ inline Scratch scratch_at(void* ws, int G, int BM, int d) {
   return s;
 }
 
-// A request: its rows of q, its new tokens (0: nothing to do), its tokens in the cache.
-struct Request {
-  int q0, len, kv;
-};
 // `top`: the largest of the offsets before request i (a range that starts below it is malformed).
 __device__ __forceinline__ Request request_of(const PagedParams& p, int i, int top, bool* bad) {
   Request r;
@@ -371,7 +374,7 @@ __device__ __forceinline__ void redo_row(const PagedParams& p, const Scratch& s,
   }
 }
 
-// Puts the partial results of shared items together (grid: G x ceil(BM / 8), 8 rows a CTA).
+// Puts the partial results of shared items together.
 cudaError_t launch_join(const PagedParams& p, int bf16, const Scratch& s, int G, int BM, int tile_tokens, cudaStream_t stream);
 cudaError_t launch_simt(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream);
 cudaError_t simt_workspace(const PagedParams& p, int bf16, size_t* bytes);
