@@ -139,15 +139,28 @@ struct Walk {
 struct PlanSmem {
   long long sum[32];
   int top[32];
-  long long start;
+  long long start, per_head;
   int req, top_before;
 };
 
+// Places of one key head's items of this lane's request.  Long chunks (more than 32 tiles) by the whole warp.
 template <int BN, int COST>
-__device__ __forceinline__ long long request_places(const PagedParams& p, const Request& r, int tile_tokens) {
+__device__ __forceinline__ long long places_of(const PagedParams& p, const Request& r, int tile_tokens) {
+  constexpr int kAlone = 32;
   long long n = 0;
-  for (int t = 0; t < r.len; t += tile_tokens) n += COST + units_of<BN>(span_of(p, r, t, tile_tokens));
-  return n * p.h_kv;
+  if (r.len <= kAlone * tile_tokens)
+    for (int t = 0; t < r.len; t += tile_tokens) n += COST + units_of<BN>(span_of(p, r, t, tile_tokens));
+  for (unsigned many = __ballot_sync(0xffffffffu, r.len > kAlone * tile_tokens); many; many &= many - 1) {
+    const int l = __ffs(many) - 1, lane = threadIdx.x & 31;
+    const Request x = {__shfl_sync(0xffffffffu, r.q0, l), __shfl_sync(0xffffffffu, r.len, l), __shfl_sync(0xffffffffu, r.kv, l)};
+    const int tiles = (x.len - 1) / tile_tokens + 1;
+    long long sum = 0;
+    for (int t = lane; t < tiles; t += 32) sum += COST + units_of<BN>(span_of(p, x, t * tile_tokens, tile_tokens));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == l) n = sum;
+  }
+  return n;
 }
 
 // Finds this CTA's stretch: false if it has none.  All NT threads of the CTA call it; CTA 0 reports
@@ -176,13 +189,13 @@ __device__ bool plan(const PagedParams& p, int tile_tokens, PlanSmem& sm, Walk<B
         if (x < warp) before = max(before, sm.top[x]);
         top = max(top, sm.top[x]);
       }
-      long long mine = 0;
+      Request r = {0, 0, -1};
       if (i < p.n) {
         bool bad;
-        const Request r = request_of(p, i, before, &bad);
-        mine = request_places<BN, COST>(p, r, tile_tokens);
+        r = request_of(p, i, before, &bad);
         if (bad && pass == 0 && blockIdx.x == 0) atomicExch(p.status, GDN_ERR_SHAPE);
       }
+      const long long per_head = places_of<BN, COST>(p, r, tile_tokens), mine = per_head * p.h_kv;
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -203,6 +216,7 @@ __device__ bool plan(const PagedParams& p, int tile_tokens, PlanSmem& sm, Walk<B
       }
       if ((pass == 1 || p.n <= NT) && mine > 0 && start <= u0 && u0 < start + mine) {
         sm.start = start;
+        sm.per_head = per_head;
         sm.req = i;
         sm.top_before = before;
       }
@@ -224,14 +238,27 @@ __device__ bool plan(const PagedParams& p, int tile_tokens, PlanSmem& sm, Walk<B
   bool bad;
   w.r = request_of(p, w.req, w.top, &bad);
   long long u = u0 - sm.start;
-  const long long per_head = request_places<BN, COST>(p, w.r, tile_tokens) / p.h_kv;
-  w.head = (int)(u / per_head);
-  u -= w.head * per_head;
-  for (w.tile = 0;; ++w.tile) {
-    w.set_tile(p, tile_tokens);
-    if (u < COST + w.units) break;
-    u -= COST + w.units;
+  w.head = (int)(u / sm.per_head);
+  u -= w.head * sm.per_head;
+  for (int first = 0;; first += 32) {  // the tile that place u lies in, 32 of them at a time
+    const int t = first + lane;
+    const int mine = t * (long long)tile_tokens < w.r.len ? COST + units_of<BN>(span_of(p, w.r, t * tile_tokens, tile_tokens)) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned there = __ballot_sync(0xffffffffu, u < incl);
+    if (there) {
+      const int l = __ffs(there) - 1;
+      w.tile = first + l;
+      u -= __shfl_sync(0xffffffffu, incl - mine, l);
+      break;
+    }
+    u -= __shfl_sync(0xffffffffu, incl, 31);
   }
+  w.set_tile(p, tile_tokens);
   w.begin = u0 - u;
   w.at = max(0, (int)u - COST);
   w.left = (int)(end - (w.begin + COST + w.at));  // (a stretch has fewer places than 2^31 units)
