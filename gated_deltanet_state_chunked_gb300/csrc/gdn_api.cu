@@ -177,8 +177,6 @@ int check_paged(const gdn_paged_dims* d, const void* q, const void* k, const voi
   p->group = d->h_q / d->h_kv; p->d = d->d; p->n_pages = d->n_pages; p->width = d->table_width; p->window = d->window;
   while ((1 << p->page_shift) < d->page_size) ++p->page_shift;
   p->scale = d->scale;
-  p->status = device_status_word();
-  if (!p->status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   return GDN_OK;
 }
 
@@ -506,6 +504,8 @@ int gdn_kv_append(const gdn_paged_dims* dims, const gdn_rotary* rotary, const vo
   if (q && q == q_out && dims->q_stride != (int64_t)dims->h_q * dims->d)
     return fail(GDN_ERR_ARG, "q_out may be q only where q has no gaps");
   p.inv_freq = inv_freq; p.positions = positions; p.k_pages = k_pages; p.v_pages = v_pages; p.O = q_out;
+  p.status = device_status_word();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   const cudaError_t e = launch_kv_append(p, dims->dtype == GDN_BF16, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gdn_kv_append launch");
   return GDN_OK;
@@ -522,6 +522,8 @@ int gdn_paged_attn(const gdn_paged_dims* dims, const void* q, const void* k_page
   if (!aligned(O_out, 16)) return fail(GDN_ERR_ALIGN, "O_out must be 16-byte aligned");
   if (!aligned(lse_out, 4)) return fail(GDN_ERR_ALIGN, "lse_out must be 4-byte aligned");
   p.O = O_out; p.lse = lse_out;
+  p.status = device_status_word();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int bf16 = dims->dtype == GDN_BF16;
   size_t bytes = 0;

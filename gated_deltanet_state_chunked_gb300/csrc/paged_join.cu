@@ -107,17 +107,29 @@ cudaError_t launch_join(const PagedParams& p, int bf16, const Scratch& s, int G,
 
 }  // namespace paged
 
-// bf16: up to 16 rows a key head (single tokens) leave 128-row products nearly empty and need bytes under way; pages that have no tensor
-// map (fewer than 8 tokens, strides that it does not take) fall to the CUDA cores, as fp32 does.
+namespace {
+
+// bf16: up to 16 rows a key head leave 128-row products nearly empty, and are bound by bytes under way (paged_split.cu);
+// more go to the tensor pipe (paged_tc.cu).  Pages that have no tensor map (fewer than 8 tokens, strides that it does not
+// take): up to 32 rows as before, more on the CUDA cores, as fp32 is (paged_simt.cu).
+enum Path { kSplit, kTensor, kCores };
+Path path_of(const PagedParams& p, int bf16) {
+  const long long rows = (long long)p.max_q * p.group;
+  if (!bf16) return kCores;
+  return rows <= 16 ? kSplit : paged::tc_supported(p) ? kTensor : rows <= 32 ? kSplit : kCores;
+}
+
+}  // namespace
+
 cudaError_t paged_workspace_bytes(const PagedParams& p, int bf16, size_t* bytes) {
-  if (bf16 && paged::split_supported(p)) return paged::split_workspace(p, bytes);
-  if (bf16 && paged::tc_supported(p)) return paged::tc_workspace(p, bytes);
-  return paged::simt_workspace(p, bf16, bytes);
+  const Path path = path_of(p, bf16);
+  return path == kSplit ? paged::split_workspace(p, bytes) : path == kTensor ? paged::tc_workspace(p, bytes) : paged::simt_workspace(p, bf16, bytes);
 }
 cudaError_t launch_paged_attn(const PagedParams& p, int bf16, void* workspace, cudaStream_t stream) {
-  if (bf16 && paged::split_supported(p)) return paged::launch_split(p, workspace, stream);
-  if (bf16 && paged::tc_supported(p)) return paged::launch_tc(p, workspace, stream);
-  return paged::launch_simt(p, bf16, workspace, stream);
+  const Path path = path_of(p, bf16);
+  return path == kSplit    ? paged::launch_split(p, workspace, stream)
+         : path == kTensor ? paged::launch_tc(p, workspace, stream)
+                           : paged::launch_simt(p, bf16, workspace, stream);
 }
 
 }  // namespace gdn

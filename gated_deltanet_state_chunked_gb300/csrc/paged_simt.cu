@@ -9,7 +9,9 @@ namespace {
 // holds rows TR ty .. and keys tx + 16 j of the scores, columns 2 tx + 32 j (and the next) of the outputs, as pairs for the
 // packed FMAs (two products in one instruction; the scores' pairs are even and odd places of the head).  Keys and values
 // each have one buffer: the next tile's keys arrive while the values are multiplied, its values while the scores are.
-// Bound by the FMA pipe: BENCH
+// Bound by the FMA pipe in long chunks (1,024 tokens over 3,000, 32 heads of 128, fp32: 1.53 ms, 38 TFLOP/s); short ones by
+// their few units on each CTA.  Single tokens (64 over up to 6,000 keys: 540 us, 3 TB/s) by shared memory, for which 16-row
+// tiles with few rows are wide: warps without rows only load (with all of them at work 914 us).
 constexpr int NT = 256, BN = 64, LDP = BN + 4;
 constexpr int COST = 0;  // (of an item, in units: a unit takes 13 us, the rest of an item 4)
 
@@ -166,33 +168,33 @@ __global__ void __launch_bounds__(NT, TR <= 2 ? 2 : 1) paged_simt_kernel(PagedPa
       cp_commit();
       if (busy) {
 #pragma unroll
-      for (int i = 0; i < TR; ++i) {
-        float top = -CUDART_INF_F;
+        for (int i = 0; i < TR; ++i) {
+          float top = -CUDART_INF_F;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = j0 + tx + 16 * j;
-          a[i][j] = key >= lo[i] && key < hi[i] ? a[i][j] * s2 : -CUDART_INF_F;
-          top = fmaxf(top, a[i][j]);
+          for (int j = 0; j < 4; ++j) {
+            const int key = j0 + tx + 16 * j;
+            a[i][j] = key >= lo[i] && key < hi[i] ? a[i][j] * s2 : -CUDART_INF_F;
+            top = fmaxf(top, a[i][j]);
+          }
+#pragma unroll
+          for (int x = 8; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          const float m_new = fmaxf(m[i], top), ref = m_new == -CUDART_INF_F ? 0.f : m_new;
+          const float shrink = exp2f(m[i] - ref);
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = exp2f(a[i][j] - ref);
+            P[(ty * TR + i) * LDP + tx + 16 * j] = e;
+            sum += e;
+          }
+#pragma unroll
+          for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          l[i] = fmaf(l[i], shrink, sum);
+          m[i] = m_new;
+          const uint64_t ss = pair(shrink, shrink);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[i][c] = mul2(o[i][c], ss);
         }
-#pragma unroll
-        for (int x = 8; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float m_new = fmaxf(m[i], top), ref = m_new == -CUDART_INF_F ? 0.f : m_new;
-        const float shrink = exp2f(m[i] - ref);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = exp2f(a[i][j] - ref);
-          P[(ty * TR + i) * LDP + tx + 16 * j] = e;
-          sum += e;
-        }
-#pragma unroll
-        for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l[i] = fmaf(l[i], shrink, sum);
-        m[i] = m_new;
-        const uint64_t ss = pair(shrink, shrink);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[i][c] = mul2(o[i][c], ss);
-      }
       }
       cp_wait<1>();
       __syncthreads();

@@ -1,9 +1,12 @@
-// gdn_paged_attn, bf16, up to 32 query rows a key head: single tokens and short windows.
+// gdn_paged_attn, bf16, up to 16 query rows a key head (32 where the pages have no tensor map): single tokens and
+// short windows.
 //
 // Bound by HBM: every key and value is read once for few rows.  So the products are small (warp-level
-// mma.sync, 16 rows x 16 keys; tcgen05 tiles of 128 rows would be nearly empty) and what counts is bytes under way: each warp
-// has a ring of five half stages (16 keys, then their 16 values) of its own that runs ahead across items, without any
-// barrier in the loop; two CTAs of four warps an SM keep 128 KB in flight and cover each other's ends of items.
+// mma.sync, 16 rows x 16 keys; tcgen05 tiles of 128 rows would be nearly empty: 128 tokens over up to 16K keys 1,057 us
+// on them) and what counts is bytes under way: each warp has a ring of five half stages (16 keys, then their 16 values) of
+// its own that runs ahead across items, without any barrier in the loop; two CTAs of four warps an SM keep 128 KB in
+// flight and cover each other's ends of items.  Measured: those 128 tokens 610 us, 6.5 TB/s.  Two 16-row tiles a warp
+// are bound by the warps' instructions: 64 windows of 20 rows 304 us, on the tcgen05 kernel 167.
 // A unit is 64 keys, 16 a warp.  Every warp carries its own maximum, sum and output rows; at an item's end they are
 // put together through shared memory, each warp finishing a quarter of the columns.
 #include "paged_work.cuh"
@@ -13,7 +16,7 @@ namespace paged {
 namespace {
 
 constexpr int NW = 4, NT = 32 * NW, BN = 16 * NW, kRing = 5;
-constexpr int COST = 2;  // of an item, in units (measured: 3.5 us against 1.4)
+constexpr int COST = 2;  // of an item, in units (3.5 us against 1.4; with 4: 128 tokens 626 us against 610)
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -375,8 +378,6 @@ cudaError_t launch(const PagedParams& p, const Scratch& s, int G, int tile_token
 int rows_of(const PagedParams& p) { return (long long)p.max_q * p.group <= 16 ? 16 : 32; }
 
 }  // namespace
-
-bool split_supported(const PagedParams& p) { return (long long)p.max_q * p.group <= 16; }
 
 cudaError_t split_workspace(const PagedParams& p, size_t* bytes) {
   int sms = 0;

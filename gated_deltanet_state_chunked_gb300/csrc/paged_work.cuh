@@ -407,7 +407,6 @@ cudaError_t launch_simt(const PagedParams& p, int bf16, void* workspace, cudaStr
 cudaError_t simt_workspace(const PagedParams& p, int bf16, size_t* bytes);
 cudaError_t launch_tc(const PagedParams& p, void* workspace, cudaStream_t stream);
 bool tc_supported(const PagedParams& p);
-bool split_supported(const PagedParams& p);
 cudaError_t launch_split(const PagedParams& p, void* workspace, cudaStream_t stream);
 cudaError_t split_workspace(const PagedParams& p, size_t* bytes);
 cudaError_t tc_workspace(const PagedParams& p, size_t* bytes);

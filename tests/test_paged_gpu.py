@@ -101,6 +101,7 @@ def test_single_tokens(dt, group, d):
 def test_pages_and_layouts(dt, page, layout):
     _run([3, 3, 3], [5, 300, 129], 4, 2, 64, page, dt, 2, cu=False, layout=layout, fused=True)
     _run([40, 1, 70], [45, 300, 129], 4, 2, 64, page, dt, 3, layout=layout, fused=True)
+    _run([5, 5, 5], [5, 300, 129], 8, 2, 96, page, dt, 3, cu=False, layout=layout)
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
