@@ -531,13 +531,17 @@ def gdn_beam_reorder(pool, slots, parents, *, layers=False, slots_out=None, stre
     _fits(n, beams, n_slots, n_layers)
     dev = _cuda_index("pool", pool)
     size = pool.element_size()
-    row, steps = 1, pool.stride()
-    for length, step in zip(reversed(pool.shape[lead:]), reversed(steps[lead:])):
-        if length != 1 and step != row:
-            raise ValueError("pool: each row must be contiguous")
-        row *= length
-    slot_step = steps[lead - 1] if n_slots > 1 else row
-    layer_step = steps[0] if layers and n_layers > 1 else row
+    if pool.is_contiguous():
+        row = pool.numel() // (n_layers * n_slots) if n_layers * n_slots else 0
+        slot_step, layer_step = row, row * n_slots
+    else:
+        row, steps = 1, pool.stride()
+        for length, step in zip(reversed(pool.shape[lead:]), reversed(steps[lead:])):
+            if length != 1 and step != row:
+                raise ValueError("pool: each row must be contiguous")
+            row *= length
+        slot_step = steps[lead - 1] if n_slots > 1 else row
+        layer_step = steps[0] if layers and n_layers > 1 else row
     i32 = torch.int32
     args = (_want("slots", slots, dev, i32, (n, beams)), _want("parents", parents, dev, i32, (n, beams)))
     _want("slots_out", slots_out, dev, i32, (n, beams))

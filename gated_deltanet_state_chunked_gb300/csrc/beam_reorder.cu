@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kReorderNT) beam_reorder_kernel(ReorderParams 
   // a slot that an earlier request names too
   for (int64_t i = tid; i < first; i += kReorderNT) {
     const int s = p.slots[i];
-    if (s >= 0)
+    if (s >= 0 && p.slots[i - i % p.beams] >= 0)  // (not those of padding)
       for (int j = 0; j < p.beams; ++j) bad = bad || slot[j] == s;
   }
   if (__syncthreads_or(bad)) {

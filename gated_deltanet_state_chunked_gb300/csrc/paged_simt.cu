@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(NT, TR <= 2 ? 2 : 1) paged_simt_kernel(PagedPa
       const Row x = row_of(p, rq, w.head, w.tile, tile_tokens, ty * TR + i);
       const int pos = rq.kv - rq.len + x.t;
       hi[i] = x.live ? pos + 1 : 0;
-      lo[i] = p.window ? max(0, pos - p.window + 1) : 0;
+      lo[i] = low_of(p, pos);
     }
     int any = 0;
 #pragma unroll

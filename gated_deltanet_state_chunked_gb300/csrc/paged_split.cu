@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(NT, 2) paged_split_kernel(const PagedParams p,
         const int pos = rq.kv - rq.len + x.t;
         // (a row that is none sees everything, so that it calls for no masking; nothing of it is stored)
         hi[t][i] = x.live ? pos + 1 : INT_MAX;
-        lo[t][i] = x.live && p.window ? max(0, pos - p.window + 1) : 0;
+        lo[t][i] = x.live ? low_of(p, pos) : 0;
         ref[t][i] = -CUDART_INF_F;
         l[t][i] = 0.f;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(rq.q0 + x.t) * p.q_stride + (int64_t)x.h * p.d;

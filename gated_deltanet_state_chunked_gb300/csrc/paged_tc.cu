@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(NT, 1)
         const Row x = row_of(p, w.r, w.head, w.tile, tile_tokens, (split ? 0 : 128 * group) + 32 * quad + lane);
         const int pos = w.r.kv - w.r.len + x.t;
         // (a row that is none sees everything, so that it calls for no masking; nothing of it is stored)
-        const int hi = x.live ? pos + 1 : INT_MAX, lo = x.live && p.window ? max(0, pos - p.window + 1) : 0;
+        const int hi = x.live ? pos + 1 : INT_MAX, lo = x.live ? low_of(p, pos) : 0;
         float ref = -CUDART_INF_F, l = 0.f;
         for (int i_u = 0; i_u < mine; ++i_u, ++done) {
           if (!(ok = wait(kS + group, done, kLongNs))) break;

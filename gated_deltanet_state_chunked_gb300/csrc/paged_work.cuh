@@ -73,6 +73,11 @@ __device__ __forceinline__ Request request_of(const PagedParams& p, int i, int t
 }
 __device__ __forceinline__ int top_of(const PagedParams& p, int i) { return p.cu ? max(p.cu[i], p.cu[i + 1]) : INT_MIN; }
 
+// The first key that position `pos` sees.
+__device__ __forceinline__ int low_of(const PagedParams& p, int pos) {
+  return p.window && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
 // Keys that the tokens [t0, t0 + n) of a request see: [lo, hi).
 struct Span {
   int lo, hi;
@@ -81,7 +86,7 @@ __device__ __forceinline__ Span span_of(const PagedParams& p, const Request& r, 
   const int base = r.kv - r.len;  // position of the first new token
   Span s;
   s.hi = max(0, min(r.kv, base + min(t0 + n, r.len)));
-  s.lo = p.window ? max(0, base + t0 - p.window + 1) : 0;
+  s.lo = low_of(p, base + t0);
   return s;
 }
 template <int BN>
@@ -384,7 +389,7 @@ template <typename T>
 __device__ __forceinline__ void redo_row(const PagedParams& p, const Scratch& s, const Request& rq, int req, int head,
                                          const Row& x, int first, int end, bool whole, size_t slot_row) {
   const int lane = threadIdx.x & 31, pos = rq.kv - rq.len + x.t;
-  const int lo = max(first, p.window ? pos - p.window + 1 : 0), hi = min(end, pos + 1);
+  const int lo = max(first, low_of(p, pos)), hi = min(end, pos + 1);
   float o[4], m, l;
   row_again<T>(p, req, head, x.h, rq.q0 + x.t, lo, hi, o, &m, &l);
   const size_t out = (size_t)(rq.q0 + x.t) * p.h_q + x.h;

@@ -425,7 +425,7 @@ typedef struct {
  * gdn_beam_reorder -- the rows of a pool (gdn_decode's states; pages of a key-value cache) follow their beams.
  * The pages have no counterpart; the call stands between gdn_beam_select and the next gdn_decode.
  *   slots       int32 device [n_seqs][beams]: the row of each beam so far.  A negative first slot: padding, its
- *               request's slots_out are -1 and nothing of it moves.
+ *               request's slots_out are -1, nothing of it moves, and what else it holds does not matter.
  *   parents     int32 device [n_seqs][beams]: the beam that each new beam continues, or negative: none (the new beam
  *               gets a slot, whose row stays as it is)
  *   pool        any rows of row_bytes, updated in place

@@ -232,7 +232,8 @@ def test_reorder_rows_of_other_types_and_strides():
 
 def test_reorder_reports_what_is_malformed():
     pool = torch.arange(40.0).reshape(10, 4).cuda()
-    for slots, parents, live in (([[0, 1], [10, 2]], [[0, 0], [0, 0]], (0,)),   # past the pool
+    for slots, parents, live in (([[-1, 1], [1, 2], [0, 99]], [[0, 0], [0, 0], [0, 0]], (1,)),  # (padding's other slots do not matter)
+                                 ([[0, 1], [10, 2]], [[0, 0], [0, 0]], (0,)),   # past the pool
                                  ([[0, 1], [3, -1]], [[0, 0], [0, 0]], (0,)),
                                  ([[0, 0], [3, 4]], [[0, 0], [1, 1]], (1,)),    # named twice
                                  ([[0, 1], [1, 4]], [[0, 0], [1, 1]], (0,)),    # an earlier request's
@@ -244,7 +245,7 @@ def test_reorder_reports_what_is_malformed():
         assert e.value.code == _lib.GDN_ERR_SHAPE
         out, want = _reorder(pool.cpu(), [slots[i] for i in live], [parents[i] for i in live], False)
         assert [got[i].tolist() for i in live] == out
-        assert all(got[i].tolist() == [-1, -1] for i in range(2) if i not in live)
+        assert all(got[i].tolist() == [-1, -1] for i in range(len(slots)) if i not in live)
         assert torch.equal(p.cpu(), want)
 
 

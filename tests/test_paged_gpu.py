@@ -116,6 +116,9 @@ def test_tokens_without_a_key(dt):
     """More new tokens than the cache holds: the first ones see nothing."""
     _run([40, 3, 1], [17, 0, 0], 4, 2, 64, 16, dt, 6)
     _run([3, 3], [2, 0], 4, 2, 64, 16, dt, 7, cu=False)
+    for window in (1, 5, 2**31 - 1):
+        _run([40, 3, 1], [17, 0, 0], 4, 2, 64, 16, dt, 6, window=window)
+        _run([3, 3], [2, 40], 4, 2, 64, 16, dt, 7, cu=False, window=window)
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
