@@ -116,9 +116,10 @@ __device__ __forceinline__ int place_of(int i) {
   return VEC * (threadIdx.x + i / VEC * kRowNT) + i % VEC;
 }
 
-// PER values a thread, in slices of up to 256 PER.  Bound by HBM where there are many rows, with several CTAs an SM so
-// that the loads of one cover the work of the others; for few rows by the chain of load, maximum, bound and ranks of one
-// slice.  VEC values to a load: 16 bytes of rows that are aligned to them (4: fp32, 8: bf16), else 1.
+// PER values a thread, in slices of up to 256 PER, four CTAs an SM so that the loads of one cover the work of the others
+// (three: 122 us for 512 rows of 131,072 fp32 values, slices of half the size: 110; this: 83, 72 of it here).  Bound there by its
+// instructions, about 24 a value, between barriers, at 55% of HBM; for few rows by the chain of load, maximum, bound and
+// ranks of one slice.  VEC values to a load: 16 bytes of rows that are aligned to them (4: fp32, 8: bf16), else 1.
 template <typename T, int PER, int VEC>
 __global__ void __launch_bounds__(kRowNT, PER > 16 ? 4 : 6) beam_rows_kernel(BeamParams p, BeamWork w) {
   constexpr int kWarps = kRowNT / 32, kGroups = 2 * kMaxBeams;
@@ -133,19 +134,20 @@ __global__ void __launch_bounds__(kRowNT, PER > 16 ? 4 : 6) beam_rows_kernel(Bea
   const int v0 = slice * w.slice_len, len = min(p.vocab - v0, w.slice_len);
   const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride + v0;
   float a[PER];
+  if (VEC > 1 && len == PER * kRowNT) {  // a whole slice: all its loads are under way before the first is looked at
+    uint4 u[PER / VEC];
 #pragma unroll
-  for (int i = 0; i < PER; i += VEC) {
-    const int v = place_of<VEC>(i);
-    if (VEC > 1 && v + VEC <= len) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + v));
-      const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < PER / VEC; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(x + place_of<VEC>(i * VEC)));
+#pragma unroll
+    for (int i = 0; i < PER / VEC; ++i) {
+      const uint32_t y[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
-        a[i + e] = __uint_as_float(sizeof(T) == 4 ? y[e % 4] : e & 1 ? y[e / 2] & 0xffff0000u : y[e / 2] << 16);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) a[i + e] = v + e < len ? load_f(x + v + e) : -CUDART_INF_F;
+        a[i * VEC + e] = __uint_as_float(sizeof(T) == 4 ? y[e % 4] : e & 1 ? y[e / 2] & 0xffff0000u : y[e / 2] << 16);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) a[i] = place_of<VEC>(i) < len ? load_f(x + place_of<VEC>(i)) : -CUDART_INF_F;
   }
   float top = -CUDART_INF_F;
 #pragma unroll

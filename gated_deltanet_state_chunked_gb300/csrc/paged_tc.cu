@@ -16,6 +16,13 @@
 // the MMAs.  13 loads Q and K, 14 V, into a ring of five 32 KB stages, by tensor copies (a page at a time, up to 128 rows of it).
 // The rows of V behind a request's end (they may hold anything) are cleared before they are handed on.  Registers are
 // moved from the last eight warps to the rows'.  Every hand-off is an mbarrier; every wait is bounded.
+//
+// Bound: in long chunks each half's chain (scores 512 clocks, weights about 1,400, their product with the values 512, three
+// hand-offs) while the other half's runs beside it, 3,300 clocks a unit of 256 rows, where the tensor pipe alone would take
+// 2,048; S = Q K^T reads shared memory at its limit.  Measured, 32/8 heads of 128: a chunk of 2,048 at the end of 32,768 keys
+// 695 us, 1.53 PFLOP/s (753 in a long run, under the board's power limit); 64 windows of 5 over up to 6,005 keys 155 us,
+// 5.3 TB/s; 12 ragged chunks of 6,007 tokens, window 1,777, 24/4 heads of 96, 152 us (an item of 15 units costs four more).
+// Multiplying P by halves took the first from 732 to 714 us, a warp each for keys and values 16-token pages from 830 to 736.
 #include <atomic>
 
 #include "paged_work.cuh"
@@ -38,7 +45,7 @@ constexpr uint32_t kQ = 0, kQAtom = 2 * kAtom, kRing = 2 * kQAtom, kBarAt = kRin
                    kStatAt = kMisc + 16, kPlanAt = kStatAt + 2 * 128 * 8, kSmem = kPlanAt + sizeof(PlanSmem);
 static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t cS = 0, cO = 256;  // TMEM columns of the halves' S (and P) and O, 128 each
-constexpr uint64_t kLongNs = 2 * kWaitNs;  // waits that rows computed again may hold up
+constexpr uint64_t kLongNs = 8 * kWaitNs;  // waits that rows computed again may hold up
 
 enum Bar { kFull = 0, kEmpty = kFull + kStages, kQFull = kEmpty + kStages, kQEmpty, kTail, kDrain, kS, kP = kS + 2 /* by columns: 0-63, 64-127 */, kO = kP + 4,
            kStat = kO + 2, kOFree = kStat + 2, kBars = kOFree + 2 };

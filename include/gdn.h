@@ -308,12 +308,12 @@ typedef struct {
   int32_t n_seqs;        /* requests */
   int32_t total_tokens;  /* rows of q, k, v and O: the requests' new tokens */
   int32_t max_q;         /* most new tokens of one request, at least 1 */
-  int32_t h_q;           /* query heads, a multiple of h_kv: query head h reads key head h / (h_q / h_kv) */
+  int32_t h_q;           /* query heads, a multiple of h_kv, at most 128 to one: head h reads key head h / (h_q / h_kv) */
   int32_t h_kv;          /* key and value heads */
   int32_t d;             /* head dim of queries, keys and values: a multiple of 8, at most 128 */
   int32_t page_size;     /* tokens of a page, a power of two */
   int32_t n_pages;       /* pages of the cache */
-  int32_t table_width;   /* entries of a request's row of the page table */
+  int32_t table_width;   /* entries of a request's row of the page table, of at most 2^31 - 1024 tokens together */
   int32_t dtype;         /* of q, k, v, the pages and O: GDN_F32 or GDN_BF16 */
   int32_t window;        /* gdn_paged_attn: a token sees the last `window` tokens, itself among them; 0: all */
   float scale;           /* gdn_paged_attn: multiplies q.k */
