@@ -349,8 +349,8 @@ typedef struct {
  *   rotary        NULL: k and q are copied as they are
  *   inv_freq      fp32 device [rotary_dim / 2]: pair i turns by the angle position * inv_freq[i]
  *   positions     int32 device [n_axes][total_tokens], or NULL (one axis): a token's place in the cache
- * A pair (a, b) becomes (a cos - b sin, b cos + a sin).  Angles are reduced in fp64, so that far positions
- * lose nothing; the rest is fp32 and rounded once to `dtype`.
+ * A pair (a, b) becomes (a cos - b sin, b cos + a sin).  Angles are reduced to a part of a turn in integers of 2^-64, so
+ * that far positions lose nothing; the rest is fp32 and rounded once to `dtype`.
  * A malformed range (as in gdn_replay), one of more than max_q tokens, a kv_lens past the table, or a page
  * outside the cache: the request (for a page, the tokens of that page) is skipped and GDN_ERR_SHAPE reported through
  * gdn_get_status.  No scratch memory; the call can be captured into a graph and replayed with new contents.  The pages overlap

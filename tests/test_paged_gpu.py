@@ -148,6 +148,15 @@ def test_scale(dt):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("page", [4, 32])
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+@pytest.mark.parametrize("window", [0, 37])
+def test_scale_of_chunks(dt, page, scale, window):
+    """A scale that makes the smallest product the largest score, in the kernels of many rows."""
+    _run([100, 30, 260], [300, 64, 250], 4, 2, 64, page, dt, 21, scale=scale, window=window)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("what", ["k", "v"])
 def test_values_that_are_no_numbers_reach_only_who_sees_them(dt, bad, what):
@@ -242,6 +251,26 @@ def test_bad_pages_are_reported():
             assert e.value.code == _lib.GDN_ERR_SHAPE
             want = ref.attend(q[new[0]:], k_pages, v_pages, table[1:], _ints([64]))
             _check_rows(O[new[0]:], None, want, _weights(q[new[0]:], k_pages, v_pages, table[1:], _ints([64])), BF16)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("page", [4, 16, 128])
+def test_bad_pages_beside_chunks(dt, page):
+    """The same in the kernels of many rows: another request's tiles lie in the same stretch of work."""
+    gen = _gen(22)
+    new, kv = [50, 70], [300, 290]
+    k_pages, v_pages, table = ref.cache(gen, kv, page, 2, 64, dt)
+    q = torch.randn(sum(new), 4, 64, generator=gen).to(dt)
+    want = ref.attend(q[50:], k_pages, v_pages, table[1:], _ints(kv[1:]))
+    weight = _weights(q[50:], k_pages, v_pages, table[1:], _ints(kv[1:]))
+    for bad in (-1, k_pages.shape[0], 1 << 30, -(1 << 31)):
+        t = table.clone()
+        t[0, 1] = bad
+        O = api.gdn_paged_attn(q.cuda(), k_pages.cuda(), v_pages.cuda(), t.cuda(), _ints(kv).cuda(), _cu(new).cuda(), max_q=70)
+        with pytest.raises(_lib.GdnError) as e:
+            api.gdn_get_status()
+        assert e.value.code == _lib.GDN_ERR_SHAPE
+        _check_rows(O[50:], None, want, weight, dt)
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
