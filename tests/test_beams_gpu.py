@@ -132,6 +132,18 @@ def test_rows_of_a_wider_array():
         api.gdn_beam_select(x.transpose(0, 1), _scores(gen, 4, 3), 5)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_select_offsets_past_32_bits(dt):
+    """Rows 2^30 values apart: what the same rows give side by side, bit by bit."""
+    gen = _gen(11)
+    n, b, V, step = 2, 2, 50000, 2**30
+    x = _logits(gen, n, b, V, dt)
+    far = torch.empty((n * b - 1) * step + V, dtype=dt, device="cuda").as_strided((n, b, V), (b * step, step, 1))
+    far.copy_(x)
+    scores = _scores(gen, n, b)
+    assert all(torch.equal(one, other) for one, other in zip(_check(x, scores, 9), api.gdn_beam_select(far, scores, 9)))
+
+
 def test_select_captured_beside_another_graph():
     gen = _gen(5)
     x, s = _logits(gen, 4, 4, 30000, F32), _scores(gen, 4, 4)
@@ -228,6 +240,19 @@ def test_reorder_rows_of_other_types_and_strides():
     api.gdn_beam_reorder(t, slots.cuda(), parents.cuda())
     assert torch.equal(t.cpu(), _reorder(tokens, slots.tolist(), parents.tolist(), False)[1])
     api.gdn_get_status()
+
+
+def test_reorder_rows_past_32_bits():
+    """Rows of 2^31 bytes and 48, the last of them behind 4 GB."""
+    pool = torch.zeros(3, 2**31 + 48, dtype=torch.uint8, device="cuda")
+    for i in range(3):
+        pool[i, ::65521] = i + 1
+        pool[i, -1] = 10 + i
+    last = pool[2].clone()
+    slots = api.gdn_beam_reorder(pool, torch.tensor([[0, 2]], dtype=torch.int32).cuda(), torch.tensor([[1, 1]], dtype=torch.int32).cuda())
+    api.gdn_get_status()
+    assert slots.tolist() == [[2, 0]]
+    assert torch.equal(pool[0], last) and torch.equal(pool[2], last) and int(pool[1, -1]) == 11 and int(pool[1, 0]) == 2
 
 
 def test_reorder_reports_what_is_malformed():

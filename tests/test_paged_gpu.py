@@ -307,6 +307,28 @@ def test_captured_and_replayed(dt):
         assert torch.equal(O, O2)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_offsets_past_32_bits(dt):
+    """A cache of more than 2^31 values: its last pages give what the same pages give in a small cache, bit by bit."""
+    gen = _gen(23)
+    kv, page, h_kv, d = [700, 300], 16, 8, 128
+    k_pages, v_pages, table = (x.cuda() for x in ref.cache(gen, kv, page, h_kv, d, dt))
+    n = k_pages.shape[0]
+    far = 2**31 // (page * h_kv * d) + 5
+    k_far, v_far = (torch.empty(far + n, page, h_kv, d, dtype=dt, device="cuda") for _ in range(2))
+    k_far[far:], v_far[far:] = k_pages, v_pages
+    for new in ([1, 1], [5, 2], [100, 40]):
+        cu, lens = _cu(new).cuda(), _ints(kv).cuda()
+        rows = torch.randn(sum(new), 3, 2 * h_kv, d, generator=gen).to(dt).cuda()
+        q, k, v = rows[:, 0], rows[:, 1, :h_kv], rows[:, 2, :h_kv]
+        freq = torch.rand(d // 2, generator=gen).cuda()
+        near, off = ([api.gdn_kv_append(k, v, *pages, t, lens, cu, q=q, inv_freq=freq), *pages, t]
+                     for pages, t in (((k_pages, v_pages), table), ((k_far, v_far), table + far)))
+        assert torch.equal(near[0], off[0]) and torch.equal(k_far[far:], k_pages) and torch.equal(v_far[far:], v_pages)
+        assert torch.equal(api.gdn_paged_attn(*near, lens, cu, max_q=max(new)), api.gdn_paged_attn(*off, lens, cu, max_q=max(new)))
+        api.gdn_get_status()
+
+
 def test_two_streams_at_once():
     gen = _gen(20)
     k_pages, v_pages, table = ref.cache(gen, [3000] * 4, 16, 2, 128, BF16)
